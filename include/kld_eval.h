@@ -450,6 +450,116 @@ kld_status kld_eval_compare_noalloc(const void* base, const void* quant, int64_t
                                     int32_t* argmax_base_out, int32_t* argmax_quant_out,
                                     kld_eval_summary* summary_out, void* stream);
 
+/*
+ * Operators around the model's vocabulary, for callers that let the compared
+ * models answer (beam search over the same logit rows) or that carry the KL
+ * gradient back to the embedding table. They take no handle and allocate
+ * nothing: everything is enqueued on `stream` of the current device (a
+ * gfx950), scratch memory is the caller's workspace, and every call may be
+ * captured into a HIP graph. A workspace is 16-byte aligned device memory of
+ * at least the size its query gives; nothing in it outlives the call's work, so
+ * one may be used again by later calls on the same stream. Calls whose work may
+ * overlap (two streams, two graphs) need one each. Device pointers must not
+ * overlap one another unless stated. Errors of every call: KLD_ERR_INVALID_ARG,
+ * KLD_ERR_RANGE past a stated limit, KLD_ERR_NO_DEVICE,
+ * KLD_ERR_UNSUPPORTED_ARCH, KLD_ERR_HIP if a launch fails; arguments are
+ * checked before anything is enqueued. Results do not depend on timing: the
+ * same inputs give the same bits.
+ *
+ * kld_eval_beam_select: one step of beam search. Item i holds n_beams beams of
+ * scores s_w = scores[i][w]; beam w's next-token logits are row
+ * i * n_beams + w of `logits`. Logits that are not finite (NaN, either
+ * infinity) are excluded tokens: they add nothing to the normaliser and are
+ * never chosen. A live beam offers every other token v at
+ * s_w + z_v - log(sum exp z); a finished beam offers only itself, as token
+ * eos_token at s_w, and its logits are not read; a beam whose score is not
+ * finite is empty and offers nothing. The n_select best of all beams together
+ * are chosen, best first, equal scores by lowest beam, then lowest id. Scores
+ * are compared as in float64 (one beam's candidates by their logits).
+ *   logits       device rows of `vocab` elements of `dtype`, row_stride
+ *                elements apart (>= vocab), n_items * n_beams of them (at most
+ *                4,194,304); any alignment of the type
+ *   n_beams      1 .. 64, n_select 1 .. 64
+ *   finished     uint8[n_items][n_beams], nonzero for a finished beam, or NULL
+ *                for none; needs an eos_token
+ *   eos_token    id that ends a beam, in [0, vocab), or -1 for none
+ *   scores_out   float32[n_items][n_select]
+ *   parents_out  int32[n_items][n_select]  the chosen candidate's beam
+ *   tokens_out   int32[n_items][n_select]  its token
+ *   finished_out uint8[n_items][n_select]  1 if the beam was finished or the
+ *                token is eos_token
+ * Where fewer candidates exist the remaining outputs are score -inf, parent -1,
+ * token -1, finished 0, which the next step, kld_eval_beam_reorder and
+ * kld_eval_embed take as an empty beam. scores_out and finished_out may be
+ * scores and finished themselves when n_select == n_beams. n_items == 0 is a
+ * no-op.
+ */
+kld_status kld_eval_beam_select_workspace(int64_t vocab, int32_t dtype, int64_t n_items, int32_t n_beams,
+                                          int32_t n_select, int64_t* bytes_out);
+
+kld_status kld_eval_beam_select(const void* logits, int32_t dtype, int64_t vocab, int64_t row_stride,
+                                int64_t n_items, int32_t n_beams, int32_t n_select, const float* scores,
+                                const uint8_t* finished, int32_t eos_token, float* scores_out,
+                                int32_t* parents_out, int32_t* tokens_out, uint8_t* finished_out,
+                                void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * Beam states (key and value caches, token histories, recurrent states) follow
+ * the chosen beams, in place: beam w of item i becomes what beam parents[i][w]
+ * was, over the item's first lengths[i] positions. A parent outside
+ * [0, n_beams) leaves its beam as it is, positions from lengths[i] on are left
+ * as they are.
+ *   states       host array of n_states device pointers, read before the call
+ *                returns; all of one geometry, none overlapping another
+ *   parents      int32[n_items][n_beams] (n_items * n_beams at most 4,194,304)
+ *   geometry     byte q of position t of outer index o of beam
+ *                r = i * n_beams + w lies at r * beam_stride + o * outer_stride
+ *                + t * position_bytes + q: [beams, heads, positions, dim] has
+ *                n_outer = heads, [beams, positions, heads, dim] has n_outer = 1;
+ *                strides in bytes, without overlap (a stride whose count is 1
+ *                is not looked at)
+ *   lengths      int32[n_items], taken into [0, n_positions], or NULL for
+ *                n_positions everywhere
+ * A count of zero is a no-op.
+ */
+kld_status kld_eval_beam_reorder(void* const* states, int32_t n_states, int64_t n_items, int32_t n_beams,
+                                 const int32_t* parents, int64_t beam_stride, int64_t n_outer, int64_t outer_stride,
+                                 int64_t n_positions, int64_t position_bytes, const int32_t* lengths, void* stream);
+
+/*
+ * Embedding lookup with scaling: out[n] = scale * table[tokens[n]], rounded
+ * once to out_dtype (nearest even). A negative id gives a zero row, an id >=
+ * vocab a NaN row (it is never used as an address).
+ *   table        device [vocab, dim] rows of table_dtype, table_stride elements
+ *                apart (>= dim); dim 1 .. 2^24
+ *   tokens       int32[n_tokens]
+ *   out          [n_tokens, dim] rows of out_dtype, out_stride elements apart
+ * Elements between the rows are left as they are. n_tokens == 0 is a no-op.
+ */
+kld_status kld_eval_embed(const void* table, int32_t table_dtype, int64_t vocab, int64_t dim, int64_t table_stride,
+                          const int32_t* tokens, int64_t n_tokens, double scale, void* out, int32_t out_dtype,
+                          int64_t out_stride, void* stream);
+
+/*
+ * Gradient of the lookup with respect to the table:
+ *   out[v] = scale * sum over { n : tokens[n] == v } of grad[n]
+ * summed in float32 in an order that depends on the tokens alone, and rounded
+ * once to out_dtype. Ids outside [0, vocab) add nothing.
+ *   grad         device [n_tokens, dim] rows of grad_dtype, grad_stride
+ *                elements apart (>= dim); n_tokens at most 4,194,304
+ *   out          [vocab, dim] rows of out_dtype, out_stride elements apart
+ *   accumulate   0: every row is written, zero where no token names it;
+ *                otherwise the sums are added to what `out` holds (rows that
+ *                no token names are left as they are)
+ * With n_tokens == 0 the rows are zeroed, or nothing is done when accumulating.
+ */
+kld_status kld_eval_embed_grad_workspace(int64_t vocab, int64_t dim, int64_t n_tokens, int64_t* bytes_out);
+
+kld_status kld_eval_embed_grad(const void* grad, int32_t grad_dtype, int64_t grad_stride, const int32_t* tokens,
+                               int64_t n_tokens, int64_t vocab, int64_t dim, double scale, void* out,
+                               int32_t out_dtype, int64_t out_stride, int32_t accumulate, void* workspace,
+                               int64_t workspace_bytes, void* stream);
+
 /* Synchronize the handle's work and free it. NULL is a no-op returning KLD_OK. */
 kld_status kld_eval_destroy(kld_eval* h);
 

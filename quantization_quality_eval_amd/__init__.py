@@ -5,6 +5,8 @@ reduced to perplexities, their ratio and the mean / RMS probability change;
 summaries over the whole evaluation or per segment; the gradient of the KL
 divergence with respect to the quantized logits; and base rows stored as
 their top-K tokens plus the rest of the mass, compared with full quant rows.
+Around the same vocabulary: beam search steps over logit rows, the beams'
+states carried along, embedding lookup with scaling and its gradient.
 
 This module is a thin ctypes binding over the C ABI in ``include/kld_eval.h``
 (``libkldeval.so``, built from ``csrc/``). It only marshals arguments: every
@@ -97,13 +99,22 @@ def load_library(build_if_missing: bool = True):
     lib.kld_eval_grad_topk.argtypes = [vp, vp, vp, i32, vp, i64, i64, ctypes.c_double, vp, i32, vp]
     lib.kld_eval_read_probe.argtypes = [vp, vp, i64, i64, i32, vp, vp, vp, vp]
     lib.kld_eval_compare_noalloc.argtypes = [vp, vp, i64, i64, i32, i32, vp, vp, vp, vp, vp, vp]
+    f64, i64p = ctypes.c_double, ctypes.POINTER(i64)
+    lib.kld_eval_beam_select_workspace.argtypes = [i64, i32, i64, i32, i32, i64p]
+    lib.kld_eval_beam_select.argtypes = [vp, i32, i64, i64, i64, i32, i32, vp, vp, i32, vp, vp, vp, vp, vp, i64, vp]
+    lib.kld_eval_beam_reorder.argtypes = [ctypes.POINTER(vp), i32, i64, i32, vp, i64, i64, i64, i64, i64, vp, vp]
+    lib.kld_eval_embed.argtypes = [vp, i32, i64, i64, i64, vp, i64, f64, vp, i32, i64, vp]
+    lib.kld_eval_embed_grad_workspace.argtypes = [i64, i64, i64, i64p]
+    lib.kld_eval_embed_grad.argtypes = [vp, i32, i64, vp, i64, i64, i64, f64, vp, i32, i64, i32, vp, i64, vp]
     lib.kld_eval_destroy.argtypes = [vp]
     for f in (lib.kld_eval_create, lib.kld_eval_rows, lib.kld_eval_rows_tokens, lib.kld_eval_reduce,
               lib.kld_eval_reduce_async,
               lib.kld_eval_reduce_tokens, lib.kld_eval_reduce_segments, lib.kld_eval_copy_lse,
               lib.kld_eval_copy_row_flags,
               lib.kld_eval_grad, lib.kld_eval_topk_compress, lib.kld_eval_rows_topk, lib.kld_eval_grad_topk,
-              lib.kld_eval_read_probe, lib.kld_eval_compare_noalloc, lib.kld_eval_destroy):
+              lib.kld_eval_read_probe, lib.kld_eval_compare_noalloc, lib.kld_eval_beam_select_workspace,
+              lib.kld_eval_beam_select, lib.kld_eval_beam_reorder, lib.kld_eval_embed,
+              lib.kld_eval_embed_grad_workspace, lib.kld_eval_embed_grad, lib.kld_eval_destroy):
         f.restype = ctypes.c_int
     lib.kld_eval_last_error.argtypes = []
     lib.kld_eval_last_error.restype = ctypes.c_char_p
@@ -260,6 +271,53 @@ def kld_eval_compare_noalloc(base: int, quant: int, vocab: int, n_rows: int, bas
                                                           kld_out or None, match_out or None, argmax_base_out or None,
                                                           argmax_quant_out or None, summary_out or None,
                                                           stream or None))
+
+
+def kld_eval_beam_select_workspace(vocab: int, dtype: int, n_items: int, n_beams: int, n_select: int) -> int:
+    n = ctypes.c_int64()
+    _check(load_library().kld_eval_beam_select_workspace(vocab, dtype, n_items, n_beams, n_select, ctypes.byref(n)))
+    return n.value
+
+
+def kld_eval_beam_select(logits: int, dtype: int, vocab: int, row_stride: int, n_items: int, n_beams: int,
+                         n_select: int, scores: int, finished: int, eos_token: int, scores_out: int, parents_out: int,
+                         tokens_out: int, finished_out: int, workspace: int, workspace_bytes: int,
+                         stream: int = 0) -> int:
+    return _check(load_library().kld_eval_beam_select(
+        logits or None, dtype, vocab, row_stride, n_items, n_beams, n_select, scores or None, finished or None,
+        eos_token, scores_out or None, parents_out or None, tokens_out or None, finished_out or None,
+        workspace or None, workspace_bytes, stream or None))
+
+
+def kld_eval_beam_reorder(states, n_items: int, n_beams: int, parents: int, beam_stride: int, n_outer: int,
+                          outer_stride: int, n_positions: int, position_bytes: int, lengths: int = 0,
+                          stream: int = 0) -> int:
+    """states: device addresses, one per state."""
+    arr = (ctypes.c_void_p * len(states))(*states)
+    return _check(load_library().kld_eval_beam_reorder(arr, len(states), n_items, n_beams, parents or None,
+                                                       beam_stride, n_outer, outer_stride, n_positions,
+                                                       position_bytes, lengths or None, stream or None))
+
+
+def kld_eval_embed(table: int, table_dtype: int, vocab: int, dim: int, table_stride: int, tokens: int, n_tokens: int,
+                   scale: float, out: int, out_dtype: int, out_stride: int, stream: int = 0) -> int:
+    return _check(load_library().kld_eval_embed(table or None, table_dtype, vocab, dim, table_stride, tokens or None,
+                                                n_tokens, float(scale), out or None, out_dtype, out_stride,
+                                                stream or None))
+
+
+def kld_eval_embed_grad_workspace(vocab: int, dim: int, n_tokens: int) -> int:
+    n = ctypes.c_int64()
+    _check(load_library().kld_eval_embed_grad_workspace(vocab, dim, n_tokens, ctypes.byref(n)))
+    return n.value
+
+
+def kld_eval_embed_grad(grad: int, grad_dtype: int, grad_stride: int, tokens: int, n_tokens: int, vocab: int,
+                        dim: int, scale: float, out: int, out_dtype: int, out_stride: int, accumulate: bool,
+                        workspace: int, workspace_bytes: int, stream: int = 0) -> int:
+    return _check(load_library().kld_eval_embed_grad(
+        grad or None, grad_dtype, grad_stride, tokens or None, n_tokens, vocab, dim, float(scale), out or None,
+        out_dtype, out_stride, int(bool(accumulate)), workspace or None, workspace_bytes, stream or None))
 
 
 def kld_eval_destroy(h: int) -> int:
@@ -596,11 +654,286 @@ def compare_tokens(base, quant, tokens, stream=None, allow_invalid: bool = False
     return kld, match, lpb, lpq, dp, summ, tsum
 
 
+# ---- operators around the model's vocabulary (no handle) ----
+
+def _device_of(t, name):
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a device tensor, got one on {t.device}")
+    return t.device
+
+
+class _Launch:
+    """The device a call works on, made current for the call, and its stream.
+    What the call allocates belongs to that stream: memory that other streams
+    let go of may still be in use there."""
+
+    def __init__(self, device, stream):
+        import torch
+        if stream is not None and stream.device != device:
+            raise ValueError(f"stream: expected a stream on {device}, got one on {stream.device}")
+        self.device, self.given = device, stream
+        self.stream = _stream_ptr(stream, device)
+        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+    def empty(self, shape, dtype):
+        import torch
+        if self.given is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(self.given):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def workspace(self, given, nbytes):
+        import torch
+        if given is None:
+            return self.empty(max(nbytes, 1), torch.uint8)
+        if given.dtype != torch.uint8 or given.device != self.device or not given.is_contiguous() \
+                or given.numel() < nbytes:
+            raise ValueError(f"workspace: expected a contiguous uint8 tensor of >= {nbytes} bytes on {self.device}")
+        return given
+
+
+def _rows_of(t, name, device, dtype=None):
+    """Row stride of a 2-d tensor whose rows are contiguous."""
+    if t.device != device:
+        raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    n, m = t.shape
+    if (m > 1 and t.stride(1) != 1) or (n > 1 and t.stride(0) < m):
+        raise ValueError(f"{name}: expected rows of contiguous elements that do not overlap")
+    return t.stride(0) if n > 1 else m
+
+
+def _as_rows(t, n, dim, name):
+    """A tensor [..., dim] as its rows, without a copy."""
+    if t.dim() == 2:
+        return t
+    try:
+        return t.view(n, dim)
+    except RuntimeError:
+        raise ValueError(f"{name}: its rows are not one stride apart, got stride {tuple(t.stride())}") from None
+
+
+def _per(t, shape, dtype, name, device):
+    """Address of a contiguous tensor of the given shape."""
+    if t.device != device:
+        raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)}, got {t.dtype} "
+                         f"{tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def beam_workspace_bytes(vocab: int, n_items: int, n_beams: int, k: int, dtype="bf16") -> int:
+    """Bytes of the workspace ``beam_select`` uses for these sizes."""
+    return kld_eval_beam_select_workspace(vocab, _dtype_code(dtype), n_items, n_beams, k)
+
+
+def beam_select(logits, scores, k=None, finished=None, eos_token: int = -1, out=None, workspace=None, stream=None):
+    """One step of beam search: the ``k`` best continuations of each item over
+    its beams and the vocabulary (k defaults to the number of beams).
+
+    ``logits`` are next-token rows [items * beams, vocab] or [items, beams,
+    vocab] (bfloat16 or float32; rows may be padded), ``scores`` float32
+    [items, beams] the beams' log-probabilities so far (-inf: an empty beam),
+    ``finished`` an optional uint8 [items, beams]. Returns (scores, parents,
+    tokens, finished), [items, k] each, best first, as the header describes for
+    kld_eval_beam_select; ``out`` gives the four tensors to write instead. With
+    ``workspace`` (a uint8 tensor of ``beam_workspace_bytes``) and ``out`` the
+    call allocates nothing."""
+    import torch
+    device = _device_of(logits, "logits")
+    if scores.dim() != 2:
+        raise ValueError("scores: expected an [items, beams] tensor")
+    items, beams = scores.shape
+    if logits.dim() == 3:
+        if logits.shape[0] != items or logits.shape[1] != beams:
+            raise ValueError(f"logits: expected [{items}, {beams}, vocab], got {tuple(logits.shape)}")
+        if items > 1 and beams > 1 and logits.stride(0) != beams * logits.stride(1):
+            raise ValueError("logits: the rows of all beams must be one stride apart")
+        rows = logits.as_strided((items * beams, logits.shape[2]),
+                                 (logits.stride(1) if beams > 1 else logits.stride(0), logits.stride(2)))
+    elif logits.dim() == 2 and logits.shape[0] == items * beams:
+        rows = logits
+    else:
+        raise ValueError(f"logits: expected [{items * beams}, vocab], got {tuple(logits.shape)}")
+    code = _dtype_code(logits.dtype)
+    vocab = rows.shape[1]
+    k = beams if k is None else int(k)
+    stride = _rows_of(rows, "logits", device)
+    shape = torch.Size((items, max(k, 0)))
+    with _Launch(device, stream) as on:
+        nbytes = kld_eval_beam_select_workspace(vocab, code, items, beams, k)
+        f32, i32, u8 = torch.float32, torch.int32, torch.uint8
+        if out is None:
+            out = (on.empty(shape, f32), on.empty(shape, i32), on.empty(shape, i32), on.empty(shape, u8))
+        elif len(out) != 4:
+            raise ValueError("out: expected (scores, parents, tokens, finished)")
+        s, p, t, f = (_per(x, shape, dt, f"out[{i}]", device) for i, (x, dt) in enumerate(zip(out, (f32, i32, i32, u8))))
+        ws = on.workspace(workspace, nbytes)
+        kld_eval_beam_select(rows.data_ptr(), code, vocab, stride, items, beams, k,
+                             _per(scores, scores.shape, f32, "scores", device),
+                             0 if finished is None else _per(finished, scores.shape, u8, "finished", device),
+                             int(eos_token), s, p, t, f, ws.data_ptr(), ws.numel(), on.stream)
+    return out
+
+
+def _state_geometry(x, length_dim, name):
+    """(outer, outer stride, positions, position bytes, beam stride) of a state
+    [beams, ...] whose positions are dimension length_dim, strides in bytes."""
+    size, strides, e = list(x.shape), list(x.stride()), x.element_size()
+    run = 1  # elements of one position, contiguous behind length_dim
+    for d in range(x.dim() - 1, length_dim, -1):
+        if size[d] != 1 and strides[d] != run:
+            raise ValueError(f"{name}: the dimensions behind length_dim must be contiguous")
+        run *= size[d]
+    if size[length_dim] > 1 and strides[length_dim] != run:
+        raise ValueError(f"{name}: the positions must follow one another")
+    outer, step = 1, 0
+    for d in range(length_dim - 1, 0, -1):
+        if size[d] == 1:
+            continue
+        if outer > 1 and strides[d] != outer * step:
+            raise ValueError(f"{name}: the dimensions between beams and positions must be one stride apart")
+        step = step if outer > 1 else strides[d]
+        outer *= size[d]
+    return outer, step * e, size[length_dim], run * e, strides[0] * e
+
+
+def beam_reorder(states, parents, lengths=None, length_dim=None, stream=None) -> None:
+    """The beams' states follow the chosen beams, in place: state row
+    i * beams + w becomes what row i * beams + parents[i, w] was (a parent of
+    -1 leaves the row as it is).
+
+    ``states``: a tensor or a sequence of tensors [items * beams, ...] of any
+    type (caches, token histories); ``parents`` int32 [items, beams], as
+    ``beam_select`` returns it with k = beams. With ``length_dim`` and
+    ``lengths`` (int32 [items]) only that dimension's first positions of each
+    item move, the rest stays as it is; the dimensions behind length_dim are
+    contiguous, the ones between the first and it one stride apart."""
+    import torch
+    states = [states] if isinstance(states, torch.Tensor) else list(states)
+    if parents.dim() != 2:
+        raise ValueError("parents: expected an [items, beams] tensor")
+    device = _device_of(parents, "parents")
+    items, beams = parents.shape
+    if (lengths is None) != (length_dim is None):
+        raise ValueError("lengths and length_dim: give both or neither")
+    groups = {}
+    for i, x in enumerate(states):
+        name = f"states[{i}]"
+        if x.device != device:
+            raise ValueError(f"{name}: expected a tensor on {device}, got {x.device}")
+        if x.dim() < 1 or x.shape[0] != items * beams:
+            raise ValueError(f"{name}: expected [{items * beams}, ...], got {tuple(x.shape)}")
+        if length_dim is None:
+            inner = x.numel() // x.shape[0] if x.numel() else 0
+            if inner and not x[0].is_contiguous():
+                raise ValueError(f"{name}: without length_dim each beam's state must be contiguous")
+            geometry = (1, 0, 1, inner * x.element_size(), x.stride(0) * x.element_size())
+        else:
+            if not 0 < length_dim < x.dim():
+                raise ValueError(f"{name}: length_dim must be one of its dimensions behind the first")
+            geometry = _state_geometry(x, length_dim, name) if x.numel() else (0, 0, 0, 0, 0)
+        groups.setdefault(geometry, []).append(x.data_ptr())
+    with _Launch(device, stream) as on:
+        pa = _per(parents, parents.shape, torch.int32, "parents", device)
+        le = 0 if lengths is None else _per(lengths, torch.Size((items,)), torch.int32, "lengths", device)
+        for (outer, step, positions, nbytes, beam), ptrs in groups.items():
+            kld_eval_beam_reorder(ptrs, items, beams, pa, beam, outer, step, positions, nbytes, le, on.stream)
+
+
+def _token_ids(tokens, device):
+    import torch
+    if tokens.device != device:
+        raise ValueError(f"tokens: expected a tensor on {device}, got {tokens.device}")
+    if tokens.dtype != torch.int32 or not tokens.is_contiguous():
+        raise ValueError("tokens: expected a contiguous int32 tensor")
+    return tokens.data_ptr()
+
+
+def _torch_dtype(code):
+    import torch
+    return torch.float32 if code == KLD_DTYPE_F32 else torch.bfloat16
+
+
+def embed(table, tokens, scale: float = 1.0, out=None, dtype=None, stream=None):
+    """Embedding lookup with scaling: scale * table[token] for every id of
+    ``tokens`` (int32, any shape); table [vocab, dim] of bfloat16 or float32.
+    A negative id gives a zero row, an id >= vocab a NaN row. Returns
+    tokens.shape + (dim,) of ``dtype`` (the table's by default), or ``out``."""
+    device = _device_of(table, "table")
+    if table.dim() != 2:
+        raise ValueError("table: expected a [vocab, dim] tensor")
+    code = _dtype_code(table.dtype)
+    stride = _rows_of(table, "table", device)
+    vocab, dim = table.shape
+    n, tk = tokens.numel(), _token_ids(tokens, device)
+    with _Launch(device, stream) as on:
+        if out is None:
+            out = on.empty((*tokens.shape, dim), _torch_dtype(code if dtype is None else _dtype_code(dtype)))
+        else:
+            if dtype is not None and out.dtype != _torch_dtype(_dtype_code(dtype)):
+                raise TypeError(f"out: expected {_torch_dtype(_dtype_code(dtype))}, got {out.dtype}")
+            if tuple(out.shape) != (*tokens.shape, dim):
+                raise ValueError(f"out: expected shape {(*tokens.shape, dim)}, got {tuple(out.shape)}")
+        rows = _as_rows(out, n, dim, "out")
+        ostride = _rows_of(rows, "out", device)
+        kld_eval_embed(table.data_ptr(), code, vocab, dim, stride, tk, n, scale, rows.data_ptr(),
+                       _dtype_code(out.dtype), ostride, on.stream)
+    return out
+
+
+def embed_grad_workspace_bytes(vocab: int, dim: int, n_tokens: int) -> int:
+    """Bytes of the workspace ``embed_grad`` uses for these sizes."""
+    return kld_eval_embed_grad_workspace(vocab, dim, n_tokens)
+
+
+def embed_grad(grad, tokens, vocab: int, scale: float = 1.0, out=None, dtype="f32", accumulate: bool = False,
+               workspace=None, stream=None):
+    """Gradient of ``embed`` with respect to its table: row v of the result is
+    scale * the sum of grad[n] over the positions n with tokens[n] == v (ids
+    outside [0, vocab) add nothing). ``grad`` is tokens.shape + (dim,),
+    bfloat16 or float32; returns [vocab, dim] of ``dtype`` (or ``out``, of its
+    own type), every row written. With ``accumulate`` the sums are added to
+    ``out``."""
+    device = _device_of(grad, "grad")
+    if grad.dim() < 1 or tuple(grad.shape[:-1]) != tuple(tokens.shape):
+        raise ValueError(f"grad: expected {tuple(tokens.shape)} + (dim,), got {tuple(grad.shape)}")
+    if accumulate and out is None:
+        raise ValueError("accumulate: needs an out to add to")
+    n, dim, vocab = tokens.numel(), grad.shape[-1], int(vocab)
+    rows = _as_rows(grad, n, dim, "grad")
+    gcode, gstride = _dtype_code(grad.dtype), _rows_of(rows, "grad", device)
+    tk = _token_ids(tokens, device)
+    with _Launch(device, stream) as on:
+        if out is None:
+            out = on.empty((vocab, dim), _torch_dtype(_dtype_code(dtype)))
+        elif tuple(out.shape) != (vocab, dim):
+            raise ValueError(f"out: expected shape {(vocab, dim)}, got {tuple(out.shape)}")
+        ostride = _rows_of(out, "out", device)
+        ws = on.workspace(workspace, kld_eval_embed_grad_workspace(vocab, dim, n))
+        kld_eval_embed_grad(rows.data_ptr(), gcode, gstride, tk, n, vocab, dim, scale, out.data_ptr(),
+                            _dtype_code(out.dtype), ostride, accumulate, ws.data_ptr(), ws.numel(), on.stream)
+    return out
+
+
 __all__ = ["Evaluator", "Summary", "TokenSummary", "compare", "compare_tokens", "KldEvalError", "kld_eval_create",
            "kld_eval_rows", "kld_eval_rows_tokens", "kld_eval_reduce", "kld_eval_reduce_tokens",
            "kld_eval_reduce_segments", "kld_eval_copy_lse", "kld_eval_copy_row_flags", "kld_eval_grad", "kld_eval_topk_compress",
            "kld_eval_rows_topk", "kld_eval_grad_topk", "kld_eval_read_probe", "read_probe", "kld_eval_destroy",
            "kld_eval_compare_noalloc", "kld_eval_reduce_async", "summary_from_bytes",
-           "kld_eval_last_error",
+           "kld_eval_last_error", "kld_eval_beam_select_workspace", "kld_eval_beam_select", "kld_eval_beam_reorder",
+           "kld_eval_embed", "kld_eval_embed_grad_workspace", "kld_eval_embed_grad", "beam_workspace_bytes",
+           "beam_select", "beam_reorder", "embed", "embed_grad_workspace_bytes", "embed_grad",
            "load_library", "build_library", "library_path", "KLD_DTYPE_F32", "KLD_DTYPE_BF16",
            "KLD_ROW_FLAG_AMPLIFIED", "KLD_ROW_FLAG_QUANT_MASS", "KLD_ROW_FLAG_CARRIED"]

@@ -1,8 +1,9 @@
 // Host side of the C ABI declared in include/kld_eval.h: handle lifetime,
 // argument validation, stream/event ordering, latched asynchronous errors and
 // the summary copy-back. All computation happens in the HIP kernels
-// (kld_row.hip, kld_reduce.hip, kld_grad.hip, kld_topk.hip; kld_probe.hip for
-// the read-bandwidth probe).
+// (kld_row.hip, kld_reduce.hip, kld_grad.hip, kld_topk.hip; kld_beam.hip,
+// kld_reorder.hip and kld_embed.hip for the operators around the model's
+// vocabulary; kld_probe.hip for the read-bandwidth probe).
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -21,6 +22,7 @@
 #include "kld_eval.h"
 #include "kld_kernels.h"
 #include "kld_probe.h"
+#include "kld_vocab.h"
 
 #ifdef KLD_EVAL_ROCTX
 #include <rocprofiler-sdk-roctx/roctx.h>
@@ -396,6 +398,109 @@ kld_status noalloc_scratch(int dev, kldk::Partial** out) {
         g_scratch_checked[dev] = true;
     }
     *out = g_scratch_ptr[dev];
+    return KLD_OK;
+}
+
+// The current device is one the kernels are built for (checked once per device).
+std::mutex g_arch_mu;
+bool g_arch_checked[kMaxDevices] = {};
+
+kld_status current_device_ok(const char* who) {
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return fail(KLD_ERR_NO_DEVICE, hip_msg(who, e));
+    if (dev < 0 || dev >= kMaxDevices)
+        return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": device index beyond the supported 64");
+    std::lock_guard<std::mutex> g(g_arch_mu);
+    if (g_arch_checked[dev]) return KLD_OK;
+    hipDeviceProp_t prop;
+    e = hipGetDeviceProperties(&prop, dev);
+    if (e != hipSuccess) return fail(KLD_ERR_HIP, hip_msg(who, e));
+    if (std::strncmp(prop.gcnArchName, "gfx950", 6) != 0)
+        return fail(KLD_ERR_UNSUPPORTED_ARCH, std::string(who) + ": built for gfx950, device is " + prop.gcnArchName);
+    g_arch_checked[dev] = true;
+    return KLD_OK;
+}
+
+bool is_dtype(int32_t d) { return d == KLD_DTYPE_F32 || d == KLD_DTYPE_BF16; }
+int64_t dtype_size(int32_t d) { return d == KLD_DTYPE_F32 ? 4 : 2; }
+bool aligned(const void* p, int64_t to) { return reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(to) == 0; }
+bool product_over(int64_t a, int64_t b, int64_t limit) { return b > 0 && a > limit / b; }
+
+// Largest extent in bytes that an array argument may span.
+constexpr int64_t kMaxExtent = int64_t{1} << 56;
+// Rows of one beam selection, beams of one reordering, positions of one embedding gradient.
+constexpr int64_t kMaxVocabRows = int64_t{1} << 22;
+constexpr int64_t kWorkspaceAlign = 16;
+
+kld_status check_workspace(const char* who, const void* ws, int64_t bytes, int64_t need) {
+    if (!ws || bytes < need)
+        return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": the workspace needs " + std::to_string(need) + " bytes");
+    if (!aligned(ws, kWorkspaceAlign))
+        return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": the workspace must be 16-byte aligned");
+    return KLD_OK;
+}
+
+kld_status check_beams(const char* who, int64_t n_items, int32_t n_beams) {
+    if (n_beams < 1 || n_beams > kldk::kBeamMaxBeams)
+        return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": n_beams must be in [1, 64]");
+    if (n_items < 0) return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": negative n_items");
+    if (product_over(n_items, n_beams, kMaxVocabRows))
+        return fail(KLD_ERR_RANGE, std::string(who) + ": n_items * n_beams exceeds 4194304");
+    return KLD_OK;
+}
+
+// Whether two states of one geometry, d > 0 bytes apart, share a byte: some
+// beam and outer index of the one lies within `inner` bytes of some of the
+// other's. The larger stride holds the whole extent of the smaller one, so the
+// nearest multiples of each decide.
+bool states_overlap(uint64_t d, int64_t rows, int64_t beam_stride, int64_t n_outer, int64_t outer_stride,
+                    int64_t inner) {
+    int64_t n1 = rows, s1 = rows > 1 ? beam_stride : 0, n2 = n_outer, s2 = n_outer > 1 ? outer_stride : 0;
+    if (s2 > s1) std::swap(n1, n2), std::swap(s1, s2);
+    if (d >= static_cast<uint64_t>(kMaxExtent) * 4) return false;
+    const int64_t dist = static_cast<int64_t>(d);
+    const int64_t k1 = s1 > 0 ? dist / s1 : 0;
+    for (int64_t a = k1; a <= k1 + (s1 > 0 ? 1 : 0) && a < n1; ++a) {
+        const int64_t left = dist - a * s1;
+        const int64_t far = left < 0 ? -left : left;
+        const int64_t k2 = s2 > 0 ? far / s2 : 0;
+        for (int64_t b = k2; b <= k2 + (s2 > 0 ? 1 : 0) && b < n2; ++b) {
+            const int64_t gap = far - b * s2;
+            if ((gap < 0 ? -gap : gap) < inner) return true;
+        }
+    }
+    return false;
+}
+
+kld_status check_beam_shape(const char* who, int32_t dtype, int64_t vocab, int64_t n_items, int32_t n_beams,
+                            int32_t n_select) {
+    if (!is_dtype(dtype))
+        return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": dtype must be KLD_DTYPE_F32 or KLD_DTYPE_BF16");
+    if (vocab < 1 || vocab > INT32_MAX)
+        return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": vocab must be in [1, 2^31-1]");
+    if (n_select < 1 || n_select > kldk::kBeamMaxSelect)
+        return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": n_select must be in [1, 64]");
+    return check_beams(who, n_items, n_beams);
+}
+
+kld_status check_table(const char* who, int64_t vocab, int64_t dim, int64_t n_tokens) {
+    if (vocab < 1 || vocab > INT32_MAX)
+        return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": vocab must be in [1, 2^31-1]");
+    if (dim < 1 || dim > (int64_t{1} << 24))
+        return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": dim must be in [1, 2^24]");
+    if (n_tokens < 0) return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": negative n_tokens");
+    return KLD_OK;
+}
+
+kld_status check_rows(const char* who, const char* what, const void* p, int32_t dtype, int64_t n, int64_t dim,
+                      int64_t stride) {
+    if (!p) return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": " + what + " is NULL");
+    if (!aligned(p, dtype_size(dtype)))
+        return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": " + what + " is not aligned to its type");
+    if (stride < dim) return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": " + what + " stride is less than a row");
+    if (product_over(n, stride, kMaxExtent / 4))
+        return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": " + what + " spans more than 2^56 bytes");
     return KLD_OK;
 }
 
@@ -887,6 +992,162 @@ kld_status kld_eval_read_probe(const void* a, const void* b, int64_t n_rows, int
         kldk::launch_read_probe(a, b, n_rows, row_bytes, waves_per_row, sink, static_cast<hipStream_t>(stream),
                                 static_cast<hipEvent_t>(start_event), static_cast<hipEvent_t>(stop_event));
     if (e != hipSuccess) return fail(KLD_ERR_HIP, hip_msg("kld_eval_read_probe: kernel launch", e));
+    return KLD_OK;
+}
+
+kld_status kld_eval_beam_select_workspace(int64_t vocab, int32_t dtype, int64_t n_items, int32_t n_beams,
+                                          int32_t n_select, int64_t* bytes_out) {
+    const CallRange range_("kld_eval_beam_select_workspace");
+    const char* who = "kld_eval_beam_select_workspace";
+    if (!bytes_out) return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": bytes_out is NULL");
+    *bytes_out = 0;
+    const kld_status st = check_beam_shape(who, dtype, vocab, n_items, n_beams, n_select);
+    if (st != KLD_OK) return st;
+    *bytes_out = kldk::beam_workspace_bytes(dtype, vocab, n_items, n_beams, n_select);
+    return KLD_OK;
+}
+
+kld_status kld_eval_beam_select(const void* logits, int32_t dtype, int64_t vocab, int64_t row_stride,
+                                int64_t n_items, int32_t n_beams, int32_t n_select, const float* scores,
+                                const uint8_t* finished, int32_t eos_token, float* scores_out,
+                                int32_t* parents_out, int32_t* tokens_out, uint8_t* finished_out,
+                                void* workspace, int64_t workspace_bytes, void* stream) {
+    const CallRange range_("kld_eval_beam_select");
+    const char* who = "kld_eval_beam_select";
+    kld_status st = check_beam_shape(who, dtype, vocab, n_items, n_beams, n_select);
+    if (st != KLD_OK) return st;
+    if (eos_token < -1 || eos_token >= vocab)
+        return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": eos_token must be -1 or in [0, vocab)");
+    if (finished && eos_token < 0)
+        return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": finished beams need an eos_token");
+    if (n_items == 0) return KLD_OK;
+    st = check_rows(who, "logits", logits, dtype, n_items * n_beams, vocab, row_stride);
+    if (st != KLD_OK) return st;
+    if (!scores || !scores_out || !parents_out || !tokens_out || !finished_out)
+        return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": scores or an output is NULL");
+    if (!aligned(scores, 4) || !aligned(scores_out, 4) || !aligned(parents_out, 4) || !aligned(tokens_out, 4))
+        return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": scores or an output is not 4-byte aligned");
+    st = check_workspace(who, workspace, workspace_bytes,
+                         kldk::beam_workspace_bytes(dtype, vocab, n_items, n_beams, n_select));
+    if (st != KLD_OK) return st;
+    st = current_device_ok(who);
+    if (st != KLD_OK) return st;
+    const kldk::BeamArgs a{logits,   dtype,     vocab,      row_stride,  n_items,    n_beams,    n_select,
+                           scores,   finished,  eos_token,  scores_out,  parents_out, tokens_out, finished_out};
+    const hipError_t e = kldk::launch_beam_select(a, workspace, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(KLD_ERR_HIP, hip_msg("kld_eval_beam_select: kernel launch", e));
+    return KLD_OK;
+}
+
+kld_status kld_eval_beam_reorder(void* const* states, int32_t n_states, int64_t n_items, int32_t n_beams,
+                                 const int32_t* parents, int64_t beam_stride, int64_t n_outer, int64_t outer_stride,
+                                 int64_t n_positions, int64_t position_bytes, const int32_t* lengths, void* stream) {
+    const CallRange range_("kld_eval_beam_reorder");
+    const char* who = "kld_eval_beam_reorder";
+    kld_status st = check_beams(who, n_items, n_beams);
+    if (st != KLD_OK) return st;
+    if (n_states < 0 || n_outer < 0 || n_positions < 0 || position_bytes < 0)
+        return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": negative count");
+    if (n_states == 0 || n_items == 0 || n_outer == 0 || n_positions == 0 || position_bytes == 0) return KLD_OK;
+    if (!states || !parents) return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": states or parents is NULL");
+    for (int32_t k = 0; k < n_states; ++k)
+        if (!states[k]) return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": a state is NULL");
+    if (!aligned(parents, 4) || !aligned(lengths, 4))
+        return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": parents or lengths is not 4-byte aligned");
+    // [beam][outer][position] without overlap, in either order of the first two
+    const int64_t rows = n_items * n_beams;
+    if (product_over(n_positions, position_bytes, kMaxExtent) ||
+        (rows > 1 && product_over(rows - 1, beam_stride, kMaxExtent)) ||
+        (n_outer > 1 && product_over(n_outer - 1, outer_stride, kMaxExtent)))
+        return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": a state spans more than 2^56 bytes");
+    const int64_t inner = n_positions * position_bytes;
+    const bool beams_outside = (n_outer == 1 || outer_stride >= inner) &&
+                               (rows == 1 || beam_stride >= (n_outer - 1) * (n_outer == 1 ? 0 : outer_stride) + inner);
+    const bool beams_inside = (rows == 1 || beam_stride >= inner) &&
+                              (n_outer == 1 || outer_stride >= (rows - 1) * (rows == 1 ? 0 : beam_stride) + inner);
+    if (!beams_outside && !beams_inside)
+        return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": the strides make beams overlap");
+    for (int32_t k = 0; k < n_states; ++k)
+        for (int32_t j = 0; j < k; ++j) {
+            const uintptr_t x = reinterpret_cast<uintptr_t>(states[k]), y = reinterpret_cast<uintptr_t>(states[j]);
+            if (states_overlap(x > y ? x - y : y - x, rows, beam_stride, n_outer, outer_stride, inner))
+                return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": two states overlap");
+        }
+    st = current_device_ok(who);
+    if (st != KLD_OK) return st;
+    const kldk::ReorderArgs a{states,  n_states,     n_items,     n_beams,        parents, beam_stride,
+                              n_outer, outer_stride, n_positions, position_bytes, lengths};
+    const hipError_t e = kldk::launch_beam_reorder(a, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(KLD_ERR_HIP, hip_msg("kld_eval_beam_reorder: kernel launch", e));
+    return KLD_OK;
+}
+
+kld_status kld_eval_embed(const void* table, int32_t table_dtype, int64_t vocab, int64_t dim, int64_t table_stride,
+                          const int32_t* tokens, int64_t n_tokens, double scale, void* out, int32_t out_dtype,
+                          int64_t out_stride, void* stream) {
+    const CallRange range_("kld_eval_embed");
+    const char* who = "kld_eval_embed";
+    if (!is_dtype(table_dtype) || !is_dtype(out_dtype))
+        return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": dtype must be KLD_DTYPE_F32 or KLD_DTYPE_BF16");
+    kld_status st = check_table(who, vocab, dim, n_tokens);
+    if (st != KLD_OK) return st;
+    if (!std::isfinite(scale)) return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": scale is not finite");
+    if (n_tokens == 0) return KLD_OK;
+    st = check_rows(who, "table", table, table_dtype, vocab, dim, table_stride);
+    if (st != KLD_OK) return st;
+    st = check_rows(who, "out", out, out_dtype, n_tokens, dim, out_stride);
+    if (st != KLD_OK) return st;
+    if (!tokens || !aligned(tokens, 4))
+        return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": tokens is NULL or not 4-byte aligned");
+    st = current_device_ok(who);
+    if (st != KLD_OK) return st;
+    const hipError_t e = kldk::launch_embed(table_dtype, out_dtype, table, vocab, dim, table_stride, tokens, n_tokens,
+                                            scale, out, out_stride, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(KLD_ERR_HIP, hip_msg("kld_eval_embed: kernel launch", e));
+    return KLD_OK;
+}
+
+kld_status kld_eval_embed_grad_workspace(int64_t vocab, int64_t dim, int64_t n_tokens, int64_t* bytes_out) {
+    const CallRange range_("kld_eval_embed_grad_workspace");
+    const char* who = "kld_eval_embed_grad_workspace";
+    if (!bytes_out) return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": bytes_out is NULL");
+    *bytes_out = 0;
+    const kld_status st = check_table(who, vocab, dim, n_tokens);
+    if (st != KLD_OK) return st;
+    if (n_tokens > kMaxVocabRows) return fail(KLD_ERR_RANGE, std::string(who) + ": n_tokens exceeds 4194304");
+    *bytes_out = kldk::embed_grad_workspace_bytes(vocab, dim, n_tokens);
+    return KLD_OK;
+}
+
+kld_status kld_eval_embed_grad(const void* grad, int32_t grad_dtype, int64_t grad_stride, const int32_t* tokens,
+                               int64_t n_tokens, int64_t vocab, int64_t dim, double scale, void* out,
+                               int32_t out_dtype, int64_t out_stride, int32_t accumulate, void* workspace,
+                               int64_t workspace_bytes, void* stream) {
+    const CallRange range_("kld_eval_embed_grad");
+    const char* who = "kld_eval_embed_grad";
+    if (!is_dtype(grad_dtype) || !is_dtype(out_dtype))
+        return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": dtype must be KLD_DTYPE_F32 or KLD_DTYPE_BF16");
+    kld_status st = check_table(who, vocab, dim, n_tokens);
+    if (st != KLD_OK) return st;
+    if (n_tokens > kMaxVocabRows) return fail(KLD_ERR_RANGE, std::string(who) + ": n_tokens exceeds 4194304");
+    if (!std::isfinite(scale)) return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": scale is not finite");
+    if (n_tokens == 0 && accumulate) return KLD_OK;
+    st = check_rows(who, "out", out, out_dtype, vocab, dim, out_stride);
+    if (st != KLD_OK) return st;
+    if (n_tokens > 0) {
+        st = check_rows(who, "grad", grad, grad_dtype, n_tokens, dim, grad_stride);
+        if (st != KLD_OK) return st;
+        if (!tokens || !aligned(tokens, 4))
+            return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": tokens is NULL or not 4-byte aligned");
+    }
+    st = check_workspace(who, workspace, workspace_bytes, kldk::embed_grad_workspace_bytes(vocab, dim, n_tokens));
+    if (st != KLD_OK) return st;
+    st = current_device_ok(who);
+    if (st != KLD_OK) return st;
+    const kldk::EmbedGradArgs a{grad, grad_dtype, grad_stride, tokens, n_tokens, vocab,
+                                dim,  scale,      out,         out_dtype, out_stride, accumulate != 0};
+    const hipError_t e = kldk::launch_embed_grad(a, workspace, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(KLD_ERR_HIP, hip_msg("kld_eval_embed_grad: kernel launch", e));
     return KLD_OK;
 }
 
