@@ -29,6 +29,7 @@ constexpr int kChunks = 4;       // 16-byte chunks per lane and tile
 constexpr int kTile = 64 * kChunks;  // chunks of a tile
 constexpr int kList = 256;       // candidates a wave holds before it must drop some
 constexpr int kMergeThreads = 256;
+constexpr int kHold = 8;         // candidates a merge thread keeps in registers
 constexpr int kMergeList = 1024;  // candidates the merge ranks at once
 
 constexpr float kLog2e = 1.44269504088896340736f;
@@ -42,7 +43,7 @@ typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 
 struct Cand {
     float z;
-    int v;
+    int v;  // -1: none
 };
 
 // Sum of a slice: sum 2^(z log2e - ref) over its finite logits. A NaN sum:
@@ -50,7 +51,7 @@ struct Cand {
 struct Slice {
     double sum;
     float ref;
-    int n;  // candidates in its list
+    int n;  // candidates found in it
 };
 
 struct Layout {
@@ -144,7 +145,10 @@ __global__ void __launch_bounds__(kWaves * 64)
                      int tiles_per_slice, int k, int drop_at, const float* __restrict__ scores,
                      const uint8_t* __restrict__ finished, Layout out) {
     constexpr int kPer = Elem<E>::kPer;
+    constexpr int kEach = kChunks * kPer;  // elements per lane and tile
     __shared__ uint64_t lists[kWaves][kList];
+    __shared__ u32x4 stages[kWaves][64 * kChunks];
+    __shared__ int owners[kWaves][64];
     const int lane = threadIdx.x & 63;
     const int64_t task = static_cast<int64_t>(blockIdx.x) * kWaves + (threadIdx.x >> 6);
     const int64_t row = task / slices;
@@ -153,6 +157,8 @@ __global__ void __launch_bounds__(kWaves * 64)
     const float score = scores[row];
     if (!isfinite(score) || (finished && finished[row])) return;  // its logits offer nothing
     uint64_t* list = lists[threadIdx.x >> 6];
+    u32x4* stage = stages[threadIdx.x >> 6];
+    int* owner = owners[threadIdx.x >> 6];
 
     // chunk c of the row: elements [c kPer - off, c kPer - off + kPer), 16-byte aligned
     const E* p = logits + row * row_stride;
@@ -202,16 +208,13 @@ __global__ void __launch_bounds__(kWaves * 64)
         const bool more = c0 + kTile < c_last;
         if (more) load(c0 + kTile, next);
 
-        float top[kChunks], best, part, to;
+        float best, part, to;
         for (bool clean = false;; clean = true) {
             best = -INFINITY;
 #pragma unroll
             for (int u = 0; u < kChunks; ++u) {
-                float m = Elem<E>::get(r[u], 0);
 #pragma unroll
-                for (int e = 1; e < kPer; ++e) m = fmaxf(m, Elem<E>::get(r[u], e));
-                top[u] = m;
-                best = fmaxf(best, m);
+                for (int e = 0; e < kPer; ++e) best = fmaxf(best, Elem<E>::get(r[u], e));
             }
             to = fmaxf(ref, best * kLog2e);
             float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -237,32 +240,36 @@ __global__ void __launch_bounds__(kWaves * 64)
             least = reached_by(best, k);
             least_key = least > -INFINITY ? static_cast<uint64_t>(order_of(least)) << 32 : 0;
         }
-        if (__ballot(best >= least && best > -INFINITY)) {
-            for (int u = 0; u < kChunks; ++u) {
-                float t = top[0];
-                u32x4 c = r[0];
+        // Lanes that hold a candidate lay their elements side by side, then the
+        // whole wave looks at them, one element per lane.
+        const bool hit = best >= least && best > -INFINITY;
+        const unsigned long long hits = __ballot(hit);
+        if (hits) {
+            if (hit) {
+                const int slot = __popcll(hits & ((1ull << lane) - 1));
+                owner[slot] = lane;
 #pragma unroll
-                for (int q = 1; q < kChunks; ++q)
-                    if (u == q) t = top[q], c = r[q];
-                if (!__ballot(t >= least && t > -INFINITY)) continue;
-                const int64_t i0 = (c0 + u * 64 + lane) * kPer - off;
-                for (int e = 0; e < kPer; ++e) {
-                    float z = Elem<E>::get(c, 0);
-#pragma unroll
-                    for (int q = 1; q < kPer; ++q)
-                        if (e == q) z = Elem<E>::get(c, q);
-                    const uint64_t key = key_of(z, static_cast<int>(i0 + e));
-                    const bool in = z > -INFINITY && key > least_key;
-                    const unsigned long long b = __ballot(in);
-                    if (!b) continue;
-                    if (in) list[n + __popcll(b & ((1ull << lane) - 1))] = key;
-                    n += __popcll(b);
-                    __builtin_amdgcn_wave_barrier();
-                    if (n > kList - 64) {
-                        n = keep_best(list, n, k, lane);
-                        least_key = list[k - 1];
-                        least = value_of(static_cast<unsigned int>(least_key >> 32));
-                    }
+                for (int u = 0; u < kChunks; ++u) stage[slot * kChunks + u] = r[u];
+            }
+            __builtin_amdgcn_wave_barrier();
+            const int held = __popcll(hits) * kEach;
+            for (int i0 = 0; i0 < held; i0 += 64) {
+                const int i = i0 + lane;
+                const int e = i % kEach;
+                const bool there = i < held;
+                const float z = there ? widen(reinterpret_cast<const E*>(stage)[i]) : -INFINITY;
+                const int64_t chunk = c0 + (e / kPer) * 64 + (there ? owner[i / kEach] : 0);
+                const uint64_t key = key_of(z, static_cast<int>(chunk * kPer + e % kPer - off));
+                const bool in = z > -INFINITY && key > least_key;
+                const unsigned long long b = __ballot(in);
+                if (!b) continue;
+                if (in) list[n + __popcll(b & ((1ull << lane) - 1))] = key;
+                n += __popcll(b);
+                __builtin_amdgcn_wave_barrier();
+                if (n > kList - 64) {
+                    n = keep_best(list, n, k, lane);
+                    least_key = list[k - 1];
+                    least = value_of(static_cast<unsigned int>(least_key >> 32));
                 }
             }
             if (n >= drop_at) {
@@ -278,10 +285,12 @@ __global__ void __launch_bounds__(kWaves * 64)
     }
 
     n = keep_best(list, n, k, lane);
-    for (int j = lane; j < n; j += 64) {
-        const uint64_t key = list[j];
-        out.cand[(row * slices + slice) * k + j] =
-            Cand{value_of(static_cast<unsigned int>(key >> 32)), static_cast<int>(0xffffffffu - static_cast<unsigned int>(key))};
+    if (lane < k) {
+        const uint64_t key = lane < n ? list[lane] : 0;
+        out.cand[(row * slices + slice) * k + lane] =
+            lane < n ? Cand{value_of(static_cast<unsigned int>(key >> 32)),
+                            static_cast<int>(0xffffffffu - static_cast<unsigned int>(key))}
+                     : Cand{-INFINITY, -1};
     }
     float whole = ref;
 #pragma unroll
@@ -318,9 +327,10 @@ __device__ __forceinline__ double value_hi(unsigned int o) {
 
 template <class E>
 __global__ void __launch_bounds__(kMergeThreads)
-    beam_merge_kernel(const E* __restrict__ logits, int64_t vocab, int64_t row_stride, int n_beams, int slices, int k,
-                      double tol, const float* scores, const uint8_t* finished, int eos, Layout in, float* scores_out,
-                      int32_t* __restrict__ parents_out, int32_t* __restrict__ tokens_out, uint8_t* finished_out) {
+    beam_merge_kernel(const E* __restrict__ logits, int64_t vocab, int64_t row_stride, int n_beams, int slices,
+                      int group, int k, double tol, const float* scores, const uint8_t* finished, int eos, Layout in,
+                      float* scores_out, int32_t* __restrict__ parents_out, int32_t* __restrict__ tokens_out,
+                      uint8_t* finished_out) {
     constexpr int kW = kMergeThreads / 64;
     enum { kEmpty, kLive, kFinished, kRetake, kExact };  // kRetake: live, its normaliser is to be taken in float64
     __shared__ float score[kBeamMaxBeams];
@@ -334,33 +344,48 @@ __global__ void __launch_bounds__(kMergeThreads)
     __shared__ int count, again;
     const int64_t item = blockIdx.x;
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    const int per = slices * k, total = n_beams * per;
+    const Cand* cands = in.cand + item * total;
+    const Slice* parts = in.slice + item * n_beams * slices;
 
-    // normalisers, one wave per beam in turn; scores and flags are read before anything is written
-    for (int w = wave; w < n_beams; w += kW) {
-        const int64_t r = item * n_beams + w;
-        const float s = scores[r];
-        const int st = !isfinite(s) ? kEmpty : finished && finished[r] ? kFinished : kLive;
+    // the first kHold candidates of a thread stay in registers
+    Cand held[kHold];
+    int beam[kHold];
+#pragma unroll
+    for (int c = 0; c < kHold; ++c) {
+        const int i = t + c * kMergeThreads;
+        beam[c] = i < total ? i / per : -1;
+        if (i < total) held[c] = cands[i];
+    }
+
+    // normalisers, `group` lanes per beam; scores and flags are read before anything is written
+    for (int w0 = 0; w0 < n_beams; w0 += kMergeThreads / group) {
+        const int w = w0 + t / group, g = t % group;
+        if (w >= n_beams) continue;
+        const float s = scores[item * n_beams + w];
+        const int st = !isfinite(s) ? kEmpty : finished && finished[item * n_beams + w] ? kFinished : kLive;
         float ref = kLeastRef;
         double sum = 0.0;
         int found = 0;
         if (st == kLive) {
-            for (int i = lane; i < slices; i += 64) {
-                const Slice q = in.slice[r * slices + i];
+            for (int i = g; i < slices; i += group) {
+                const Slice q = parts[w * slices + i];
                 const float to = fmaxf(ref, q.ref);
-                sum = sum * exp2(static_cast<double>(ref) - to) + q.sum * exp2(static_cast<double>(q.ref) - to);
+                sum = sum * static_cast<double>(__builtin_amdgcn_exp2f(ref - to)) +
+                      q.sum * static_cast<double>(__builtin_amdgcn_exp2f(q.ref - to));
                 ref = to;
                 found |= q.n;
             }
             float to = ref;
-#pragma unroll
-            for (int o = 32; o >= 1; o >>= 1) to = fmaxf(to, __shfl_xor(to, o));
-            sum *= exp2(static_cast<double>(ref) - to);
+            for (int o = group >> 1; o >= 1; o >>= 1) to = fmaxf(to, __shfl_xor(to, o));
+            sum *= static_cast<double>(__builtin_amdgcn_exp2f(ref - to));
             ref = to;
-#pragma unroll
-            for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o);
-            found = __ballot(found != 0) != 0;
+            for (int o = group >> 1; o >= 1; o >>= 1) {
+                sum += __shfl_xor(sum, o);
+                found |= __shfl_xor(found, o);
+            }
         }
-        if (lane == 0) {
+        if (g == 0) {
             score[w] = s;
             // a sum below 1/2 never reached its reference: all of the row lies below kLeastRef
             const bool sound = sum > 0.5;
@@ -370,32 +395,33 @@ __global__ void __launch_bounds__(kMergeThreads)
     }
     __syncthreads();
 
-    const int per = slices * k;
-    const auto candidate = [&](int i, Scored& c) {  // i of n_beams x slices x k; false: there is none
-        const int w = i / per, q = i - w * per;
+    const auto scored = [&](int i, int w, const Cand& x, Scored& c) {  // false: there is no such candidate
         const int st = state[w];
-        if (st == kEmpty) return false;
         if (st == kFinished) {
-            if (q != 0) return false;
             c = Scored{static_cast<double>(score[w]), 0.0f, w, eos};
-            return true;
+            return i == w * per;
         }
-        const int64_t at = (item * n_beams + w) * slices + q / k;
-        if (q % k >= in.slice[at].n) return false;
-        const Cand x = in.cand[at * k + q % k];
         c = Scored{score[w] + (static_cast<double>(x.z) - lse[w]), x.z, w, x.v};
-        return true;
+        return st != kEmpty && x.v >= 0;
     };
-    const int total = n_beams * per;
+    const auto each = [&](auto&& f) {
+        Scored c;
+#pragma unroll
+        for (int q = 0; q < kHold; ++q)
+            if (beam[q] >= 0 && scored(t + q * kMergeThreads, beam[q], held[q], c)) f(c);
+        for (int i = t + kHold * kMergeThreads; i < total; i += kMergeThreads)
+            if (scored(i, i / per, cands[i], c)) f(c);
+    };
 
     // Every further round has taken at least one more row in float64.
     for (;;) {
         for (int w = 0; w < n_beams; ++w) {
             if (state[w] != kRetake) continue;
-            const int64_t r = item * n_beams + w;
             float m = -INFINITY;
-            for (int i = t; i < slices; i += kMergeThreads)
-                if (in.slice[r * slices + i].n) m = fmaxf(m, in.cand[(r * slices + i) * k].z);
+            for (int i = t; i < slices; i += kMergeThreads) {
+                const Cand c = cands[(w * slices + i) * k];
+                if (c.v >= 0) m = fmaxf(m, c.z);
+            }
 #pragma unroll
             for (int o = 32; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
             __syncthreads();
@@ -403,7 +429,7 @@ __global__ void __launch_bounds__(kMergeThreads)
             __syncthreads();
             for (int q = 0; q < kW; ++q) m = fmaxf(m, static_cast<float>(dred[q]));
             double sum = 0.0;
-            const E* p = logits + r * row_stride;
+            const E* p = logits + (item * n_beams + w) * row_stride;
             for (int64_t i = t; i < vocab; i += kMergeThreads) {
                 const float z = widen(p[i]);
                 if (isfinite(z)) sum += exp(static_cast<double>(z) - m);
@@ -424,48 +450,51 @@ __global__ void __launch_bounds__(kMergeThreads)
 
         // a score that k candidates reach, then the candidates near or above it
         double mine = -INFINITY;
-        for (int i = t; i < total; i += kMergeThreads) {
-            Scored c;
-            if (candidate(i, c)) mine = fmax(mine, c.s);
-        }
-        const unsigned int o = order_hi(mine);
+        each([&](const Scored& c) { mine = fmax(mine, c.s); });
+        const unsigned int o = mine > -INFINITY ? order_hi(mine) : 0;
         unsigned int b = 0;
-        for (int bit = 31; bit >= 0; --bit) {
+#pragma unroll
+        for (int bit = 31; bit >= 8; --bit) {
             const unsigned int c = b | (1u << bit);
-            if (__popcll(__ballot(mine > -INFINITY && o >= c)) >= k) b = c;
+            if (__popcll(__ballot(o >= c)) >= k) b = c;
         }
         if (lane == 0) bound[wave] = b;
         if (t == 0) count = again = 0;
         __syncthreads();
         b = 0;
+#pragma unroll
         for (int q = 0; q < kW; ++q) b = bound[q] > b ? bound[q] : b;
         const double least = b ? value_hi(b) - tol : -INFINITY;
-        for (int i = t; i < total; i += kMergeThreads) {
-            Scored c;
-            if (candidate(i, c) && c.s >= least) {
+        each([&](const Scored& c) {
+            if (c.s >= least) {
                 const int at = atomicAdd(&count, 1);
                 if (at < kMergeList) list[at] = c;
             }
-        }
+        });
         __syncthreads();
         const int n = count;
-        int m = n < k + 1 ? n : k + 1;
+        const int m = n < k + 1 ? n : k + 1;
         if (n <= kMergeList) {
-            for (int i = t; i < n; i += kMergeThreads) {
-                const Scored c = list[i];
+            for (int i0 = 0; i0 < n; i0 += kMergeThreads / 4) {  // four lanes per candidate
+                const int i = i0 + (t >> 2);
                 int rank = 0;
-                for (int j = 0; j < n; ++j) rank += before(list[j], c);
-                if (rank < m) ranked[rank] = c;
+                Scored c{};
+                if (i < n) {
+                    c = list[i];
+                    for (int j = t & 3; j < n; j += 4) rank += before(list[j], c);
+                }
+                rank += __shfl_xor(rank, 1);
+                rank += __shfl_xor(rank, 2);
+                if (i < n && (t & 3) == 0 && rank < m) ranked[rank] = c;
             }
         } else {
             // too many near one another (long ties): one after the other
             const Scored none{-INFINITY, -INFINITY, 0x7fffffff, 0x7fffffff};
             for (int j = 0; j < m; ++j) {
                 Scored best = none;
-                for (int i = t; i < total; i += kMergeThreads) {
-                    Scored c;
-                    if (candidate(i, c) && (j == 0 || before(ranked[j - 1], c)) && before(c, best)) best = c;
-                }
+                each([&](const Scored& c) {
+                    if ((j == 0 || before(ranked[j - 1], c)) && before(c, best)) best = c;
+                });
 #pragma unroll
                 for (int d = 32; d >= 1; d >>= 1) {
                     const Scored other{__shfl_xor(best.s, d), __shfl_xor(best.z, d), __shfl_xor(best.w, d),
@@ -493,11 +522,10 @@ __global__ void __launch_bounds__(kMergeThreads)
         if (!again) break;
     }
 
-    const int have = count < k ? count : k;
-    for (int j = t; j < k; j += kMergeThreads) {
-        const int64_t at = item * k + j;
-        const bool some = j < have;
-        const Scored c = ranked[some ? j : 0];
+    if (t < k) {
+        const int64_t at = item * k + t;
+        const bool some = t < count;
+        const Scored c = ranked[some ? t : 0];
         scores_out[at] = some ? static_cast<float>(c.s) : -INFINITY;
         parents_out[at] = some ? c.w : -1;
         tokens_out[at] = some ? c.v : -1;
@@ -544,8 +572,10 @@ hipError_t launch_typed(const BeamArgs& a, void* workspace, hipStream_t stream) 
     // a sum of 8 and 2 more additions by 2^-24 each, log2 e by 2^-26 of the
     // entropy.
     const double tol = 2.0 * 0x1p-24 * (24.0 + log2(static_cast<double>(a.vocab)));
+    int group = 1;  // lanes that join one beam's slices
+    while (group < sh.slices && group < 64) group *= 2;
     beam_merge_kernel<E><<<dim3(static_cast<unsigned>(a.n_items)), kMergeThreads, 0, stream>>>(
-        logits, a.vocab, a.row_stride, a.n_beams, sh.slices, a.n_select, tol, a.scores, a.finished, a.eos, lay,
+        logits, a.vocab, a.row_stride, a.n_beams, sh.slices, group, a.n_select, tol, a.scores, a.finished, a.eos, lay,
         a.scores_out, a.parents_out, a.tokens_out, a.finished_out);
     return hipGetLastError();
 }
