@@ -5,13 +5,17 @@
 //
 // Gradient: dtable[v] = scale * sum over { n : t_n = v } of grad[n]. A sort of
 // the positions by their id makes each row's sum one run of the sorted order,
-// added up in the order of the positions, so results do not depend on timing:
+// added up in an order that depends on the tokens alone:
 //   1. group: wave p of P owns the ids v with v mod P = p. It reads every id,
 //      counts its own and the ones of the waves before it, and writes its
 //      positions grouped by id, each id's in increasing order. No wave waits
 //      for another.
-//   2. one workgroup per run and column tile adds the run's rows in float32.
-//   3. rows of the table that no position names are set to zero.
+//   2. sum: the sorted order is cut into pieces of kPiece positions; a workgroup
+//      adds up the runs of one piece for one tile of columns. A run that lies
+//      in the piece is done; of a run that reaches past it the piece's part is
+//      kept in float32. Further workgroups of the launch set the rows that no
+//      position names to zero.
+//   3. join: the parts of each run that was cut, in order.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -53,13 +57,18 @@ __global__ void __launch_bounds__(kThreads)
 
 // ---- gradient ----
 
+constexpr int kPiece = 32;    // positions per workgroup of the sum
+constexpr int kAhead = 8;     // rows in flight per thread
+
 struct GradSpace {
     int32_t* total;    // positions with a valid id
     int32_t* perm;     // n_tokens: positions grouped by id
-    int32_t* word;     // n_tokens: their ids
+    int32_t* word;     // n_tokens + 1: their ids, then -1
     int32_t* count;    // P * owned: positions of id p + P j at [p * owned + j]
+    float* part;       // [pieces][2][dim]: a piece's part of the run that enters it, of the run that leaves it
     int lg;            // log2 P
     int owned;         // ids per wave
+    int pieces;
 };
 
 int group_lg(int64_t vocab) {
@@ -70,21 +79,23 @@ int group_lg(int64_t vocab) {
 
 int64_t align16(int64_t b) { return (b + 15) & ~int64_t{15}; }
 
-GradSpace grad_space(void* ws, int64_t vocab, int64_t n_tokens, int64_t* bytes) {
+GradSpace grad_space(void* ws, int64_t vocab, int64_t dim, int64_t n_tokens, int64_t* bytes) {
     GradSpace g{};
     g.lg = group_lg(vocab);
     g.owned = static_cast<int>((vocab + (int64_t{1} << g.lg) - 1) >> g.lg);
+    g.pieces = static_cast<int>((n_tokens + kPiece - 1) / kPiece);
     char* p = static_cast<char*>(ws);
     int64_t at = 0;
     const auto take = [&](int64_t n) {
-        int32_t* q = reinterpret_cast<int32_t*>(p + at);
-        at += align16(n * static_cast<int64_t>(sizeof(int32_t)));
+        char* q = p + at;
+        at += align16(n * 4);
         return q;
     };
-    g.total = take(1);
-    g.perm = take(n_tokens);
-    g.word = take(n_tokens);
-    g.count = take(static_cast<int64_t>(g.owned) << g.lg);
+    g.total = reinterpret_cast<int32_t*>(take(1));
+    g.perm = reinterpret_cast<int32_t*>(take(n_tokens));
+    g.word = reinterpret_cast<int32_t*>(take(n_tokens + 1));
+    g.count = reinterpret_cast<int32_t*>(take(static_cast<int64_t>(g.owned) << g.lg));
+    g.part = reinterpret_cast<float*>(take(2 * g.pieces * ((dim + 3) & ~int64_t{3})));
     if (bytes) *bytes = at;
     return g;
 }
@@ -131,7 +142,10 @@ __global__ void __launch_bounds__(kThreads)
         sum += __shfl(incl, 63);
     }
     __builtin_amdgcn_wave_barrier();
-    if (p == mask && lane == 0) *g.total = sum;
+    if (p == mask && lane == 0) {
+        *g.total = sum;
+        g.word[sum] = -1;
+    }
     for (int64_t b = 0; b < n_tokens; b += 64) {
         const int64_t n = b + lane;
         const int32_t t = n < n_tokens ? tokens[n] : -1;
@@ -155,52 +169,179 @@ __global__ void __launch_bounds__(kThreads)
     }
 }
 
+// V consecutive elements as one load or store (V * sizeof(E) is 2 to 16 bytes).
+template <class E, int V>
+struct alignas(V * sizeof(E)) Vec {
+    E x[V];
+};
+
 template <class EG, class EO>
-__global__ void __launch_bounds__(kThreads)
-    run_sum_kernel(const EG* __restrict__ grad, int64_t grad_stride, int64_t dim, double scale, GradSpace g,
-                   EO* __restrict__ out, int64_t out_stride, bool accumulate) {
-    const int64_t i = blockIdx.x;
-    const int64_t total = *g.total;
-    if (i >= total) return;
-    const int32_t t = g.word[i];
-    if (i > 0 && g.word[i - 1] == t) return;
-    EO* o = out + t * out_stride;
-    for (int64_t c = threadIdx.x; c < dim; c += kThreads) {
-        float acc = 0.0f;
-        for (int64_t k = i; k < total && g.word[k] == t; ++k) acc += widen(grad[g.perm[k] * grad_stride + c]);
-        double x = static_cast<double>(acc) * scale;
-        if (accumulate) x += static_cast<double>(widen(o[c]));
-        put(o + c, static_cast<float>(x));
+struct GradIn {
+    const EG* grad;
+    int64_t grad_stride;
+    int64_t dim;
+    double scale;
+    EO* out;
+    int64_t out_stride;
+    int64_t vocab;
+    bool accumulate;
+};
+
+// A finished sum into its row: scaled in float64, added to what is there when
+// accumulating, rounded once.
+template <class EG, class EO, int V, class S>
+__device__ __forceinline__ void finish(const GradIn<EG, EO>& a, int32_t word, int64_t col, const S (&acc)[V]) {
+    Vec<EO, V>* o = reinterpret_cast<Vec<EO, V>*>(a.out + word * a.out_stride + col);
+    Vec<EO, V> v{};
+    if (a.accumulate) v = *o;
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        double s = static_cast<double>(acc[e]) * a.scale;
+        if (a.accumulate) s += static_cast<double>(widen(v.x[e]));
+        put(&v.x[e], static_cast<float>(s));
+    }
+    *o = v;
+}
+
+// How a launch covers rows and columns: `lanes` threads (a power of two from 64
+// to kThreads) of V elements each take one tile of a row's columns, tile after
+// tile, row unit after row unit (pieces of the sorted order, then groups of
+// rows to zero); `first`: the launch's first workgroup.
+struct Cover {
+    int64_t first;
+    int lanes;
+    int tiles;
+    int zero_rows;
+};
+struct Place {
+    int64_t unit;
+    int64_t col;
+};
+template <int V>
+__device__ __forceinline__ Place place_of(const Cover& c) {
+    const int64_t i = (c.first + blockIdx.x) * (kThreads / c.lanes) + threadIdx.x / c.lanes;
+    return Place{i / c.tiles, (i % c.tiles * c.lanes + threadIdx.x % c.lanes) * V};
+}
+
+template <class EG, class EO, int V>
+__global__ void __launch_bounds__(kThreads) run_sum_kernel(GradIn<EG, EO> a, GradSpace g, Cover c) {
+    const Place at = place_of<V>(c);
+    const int64_t piece = at.unit, col = at.col;
+    if (col >= a.dim) return;
+    if (piece >= g.pieces) {
+        if (a.accumulate) return;  // the last workgroup may reach past the pieces
+        const int64_t mask = (int64_t{1} << g.lg) - 1;
+        const int64_t v0 = (piece - g.pieces) * c.zero_rows;
+        const int64_t v1 = v0 + c.zero_rows < a.vocab ? v0 + c.zero_rows : a.vocab;
+        for (int64_t v = v0; v < v1; ++v)
+            if (g.count[(v & mask) * g.owned + (v >> g.lg)] == 0)
+                *reinterpret_cast<Vec<EO, V>*>(a.out + v * a.out_stride + col) = Vec<EO, V>{};
+        return;
+    }
+    const int total = *g.total;
+    const int i0 = static_cast<int>(piece) * kPiece;
+    if (i0 >= total) return;
+    const int i1 = i0 + kPiece < total ? i0 + kPiece : total;
+    const int64_t wide = (a.dim + 3) & ~int64_t{3};
+    bool entered = i0 > 0 && g.word[i0 - 1] == g.word[i0];
+    float acc[V] = {};
+    for (int i = i0; i < i1; i += kAhead) {
+        Vec<EG, V> row[kAhead];
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q)
+            if (i + q < i1) row[q] = *reinterpret_cast<const Vec<EG, V>*>(a.grad + g.perm[i + q] * a.grad_stride + col);
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q) {
+            if (i + q >= i1) break;
+#pragma unroll
+            for (int e = 0; e < V; ++e) acc[e] += widen(row[q].x[e]);
+            const int32_t word = g.word[i + q];
+            const bool ends = g.word[i + q + 1] != word;
+            if (!ends && i + q + 1 < i1) continue;
+            if (ends && !entered) {
+                finish<EG, EO, V>(a, word, col, acc);
+            } else {
+                float* to = g.part + (piece * 2 + (entered ? 0 : 1)) * wide + col;
+#pragma unroll
+                for (int e = 0; e < V; ++e) to[e] = acc[e];
+            }
+            entered = false;
+#pragma unroll
+            for (int e = 0; e < V; ++e) acc[e] = 0.0f;
+        }
     }
 }
 
-template <class EO>
-__global__ void __launch_bounds__(kThreads)
-    zero_rows_kernel(int64_t vocab, int64_t dim, GradSpace g, EO* __restrict__ out, int64_t out_stride) {
-    const int64_t mask = (int64_t{1} << g.lg) - 1;
-    for (int64_t v = blockIdx.x; v < vocab; v += gridDim.x) {
-        if (g.count[(v & mask) * g.owned + (v >> g.lg)] != 0) continue;
-        for (int64_t c = threadIdx.x; c < dim; c += kThreads) put(out + v * out_stride + c, 0.0f);
+// Runs that leave the piece they begin in: their parts added in order, in
+// float64.
+template <class EG, class EO, int V>
+__global__ void __launch_bounds__(kThreads) run_join_kernel(GradIn<EG, EO> a, GradSpace g, Cover c) {
+    const Place at = place_of<V>(c);
+    const int64_t piece = at.unit, col = at.col;
+    const int64_t total = *g.total, i0 = piece * kPiece, i1 = i0 + kPiece;
+    if (i1 >= total || col >= a.dim) return;
+    const int32_t word = g.word[i1 - 1];
+    if (g.word[i1] != word) return;                                     // no run leaves this piece
+    if (g.word[i0] == word && i0 > 0 && g.word[i0 - 1] == word) return;  // it began before
+    const int64_t wide = (a.dim + 3) & ~int64_t{3};
+    double sum[V];
+    const float* from = g.part + (piece * 2 + 1) * wide + col;
+#pragma unroll
+    for (int e = 0; e < V; ++e) sum[e] = from[e];
+    for (int64_t q = piece + 1; q * kPiece < total && g.word[q * kPiece] == word; ++q) {
+        const float* p = g.part + q * 2 * wide + col;
+#pragma unroll
+        for (int e = 0; e < V; ++e) sum[e] += p[e];
     }
+    finish<EG, EO, V>(a, word, col, sum);
+}
+
+template <class EG, class EO, int V>
+hipError_t grad_vec(const EmbedGradArgs& a, const GradSpace& g, hipStream_t s) {
+    const GradIn<EG, EO> in{static_cast<const EG*>(a.grad), a.grad_stride, a.dim,   a.scale,
+                            static_cast<EO*>(a.out),        a.out_stride,  a.vocab, a.accumulate};
+    Cover c{0, 64, 1, 8};
+    while (c.lanes < kThreads && int64_t{c.lanes} * V < a.dim) c.lanes *= 2;
+    c.tiles = static_cast<int>((a.dim + int64_t{c.lanes} * V - 1) / (int64_t{c.lanes} * V));
+    const int64_t zero_units = a.accumulate ? 0 : (a.vocab + c.zero_rows - 1) / c.zero_rows;
+    const int64_t per = max_blocks_per_launch(kThreads);
+    const auto blocks_of = [&](int64_t units) {
+        const int64_t in_block = kThreads / c.lanes;
+        return (units * c.tiles + in_block - 1) / in_block;
+    };
+    int64_t n = blocks_of(g.pieces + zero_units);
+    for (c.first = 0; c.first < n; c.first += per) {
+        run_sum_kernel<EG, EO, V><<<dim3(static_cast<unsigned>(n - c.first < per ? n - c.first : per)), kThreads, 0, s>>>(
+            in, g, c);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    n = blocks_of(g.pieces - 1);
+    for (c.first = 0; c.first < n; c.first += per) {
+        run_join_kernel<EG, EO, V><<<dim3(static_cast<unsigned>(n - c.first < per ? n - c.first : per)), kThreads, 0, s>>>(
+            in, g, c);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 template <class EG, class EO>
 hipError_t grad_typed(const EmbedGradArgs& a, const GradSpace& g, hipStream_t s) {
     group_kernel<<<dim3(static_cast<unsigned>((int64_t{1} << g.lg) / (kThreads / 64))), kThreads, 0, s>>>(
         a.tokens, a.n_tokens, a.vocab, g);
-    hipError_t e = hipGetLastError();
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    if (!a.accumulate) {
-        zero_rows_kernel<EO><<<dim3(static_cast<unsigned>(a.vocab < 16384 ? a.vocab : 16384)), kThreads, 0, s>>>(
-            a.vocab, a.dim, g, static_cast<EO*>(a.out), a.out_stride);
-        e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
-    if (a.n_tokens > 0)
-        run_sum_kernel<EG, EO><<<dim3(static_cast<unsigned>(a.n_tokens)), kThreads, 0, s>>>(
-            static_cast<const EG*>(a.grad), a.grad_stride, a.dim, a.scale, g, static_cast<EO*>(a.out), a.out_stride,
-            a.accumulate);
-    return hipGetLastError();
+    // widest access that both arrays' rows allow, 16 bytes of the wider type
+    constexpr int kMost = sizeof(EG) + sizeof(EO) == 4 ? 8 : 4;
+    const auto allows = [&](int v) {
+        return a.dim % v == 0 && a.grad_stride % v == 0 && a.out_stride % v == 0 &&
+               reinterpret_cast<uintptr_t>(a.grad) % (v * sizeof(EG)) == 0 &&
+               reinterpret_cast<uintptr_t>(a.out) % (v * sizeof(EO)) == 0;
+    };
+    if (allows(kMost)) return grad_vec<EG, EO, kMost>(a, g, s);
+    if (allows(2)) return grad_vec<EG, EO, 2>(a, g, s);
+    return grad_vec<EG, EO, 1>(a, g, s);
 }
 
 template <class ET, class EO>
@@ -232,14 +373,14 @@ hipError_t launch_embed(int table_type, int out_type, const void* table, int64_t
                : embed_typed<float, float>(table, vocab, dim, table_stride, tokens, n_tokens, scale, out, out_stride, s);
 }
 
-int64_t embed_grad_workspace_bytes(int64_t vocab, int64_t, int64_t n_tokens) {
+int64_t embed_grad_workspace_bytes(int64_t vocab, int64_t dim, int64_t n_tokens) {
     int64_t bytes = 0;
-    (void)grad_space(nullptr, vocab, n_tokens, &bytes);
+    (void)grad_space(nullptr, vocab, dim, n_tokens, &bytes);
     return bytes;
 }
 
 hipError_t launch_embed_grad(const EmbedGradArgs& a, void* workspace, hipStream_t s) {
-    const GradSpace g = grad_space(workspace, a.vocab, a.n_tokens, nullptr);
+    const GradSpace g = grad_space(workspace, a.vocab, a.dim, a.n_tokens, nullptr);
     if (a.grad_type == kBF16)
         return a.out_type == kBF16 ? grad_typed<uint16_t, uint16_t>(a, g, s) : grad_typed<uint16_t, float>(a, g, s);
     return a.out_type == kBF16 ? grad_typed<float, uint16_t>(a, g, s) : grad_typed<float, float>(a, g, s);
