@@ -6,10 +6,11 @@
 // Gradient: dtable[v] = scale * sum over { n : t_n = v } of grad[n]. A sort of
 // the positions by their id makes each row's sum one run of the sorted order,
 // added up in an order that depends on the tokens alone:
-//   1. group: wave p of P owns the ids v with v mod P = p. It reads every id,
-//      counts its own and the ones of the waves before it, and writes its
-//      positions grouped by id, each id's in increasing order. No wave waits
-//      for another.
+//   1. group: the positions grouped by id, each id's in increasing order. Few
+//      positions: wave p of P owns the ids v with v mod P = p; it reads every
+//      id, counts its own and the ones of the waves before it, and writes its
+//      positions; no wave waits for another. More: a counting sort by v mod P
+//      first (count, scatter), after which a workgroup sorts one residue's.
 //   2. sum: the sorted order is cut into pieces of kPiece positions; a workgroup
 //      adds up the runs of one piece for one tile of columns. A run that lies
 //      in the piece is done; of a run that reaches past it the piece's part is
@@ -59,29 +60,43 @@ __global__ void __launch_bounds__(kThreads)
 
 constexpr int kPiece = 32;    // positions per workgroup of the sum
 constexpr int kAhead = 8;     // rows in flight per thread
+static_assert(kPiece <= 64, "a lane per position");
+
+// The counting sort of many positions.
+constexpr int kLgBuckets = 10;
+constexpr int kBuckets = 1 << kLgBuckets;
+constexpr int kBucketIds = 1024;      // ids of one bucket at most
+constexpr int kSortThreads = 1024;
+constexpr int kMostChunks = 64;       // workgroups of its first two launches
+constexpr int64_t kChunkTokens = 2048;  // positions of one of them at least
+constexpr int64_t kFewTokens = 2048;    // up to here every wave reads every id
 
 struct GradSpace {
     int32_t* total;    // positions with a valid id
     int32_t* perm;     // n_tokens: positions grouped by id
     int32_t* word;     // n_tokens + 1: their ids, then -1
-    int32_t* count;    // P * owned: positions of id p + P j at [p * owned + j]
+    int32_t* count;    // positions of id v at [(v mod P) * owned + v / P]
     float* part;       // [pieces][2][dim]: a piece's part of the run that enters it, of the run that leaves it
     int lg;            // log2 P
-    int owned;         // ids per wave
+    int owned;         // ids per residue
     int pieces;
+    // counting sort only (chunks > 0)
+    int chunks;
+    int64_t chunk_tokens;
+    int32_t* hist;     // [chunks][kBuckets]
+    int32_t* start;    // kBuckets + 1: where each bucket begins
+    int32_t* bperm;    // n_tokens: positions by bucket
+    int32_t* bword;    // n_tokens: their ids
 };
-
-int group_lg(int64_t vocab) {
-    int lg = 10;
-    while ((int64_t{kOwned} << lg) < vocab) ++lg;
-    return lg;
-}
 
 int64_t align16(int64_t b) { return (b + 15) & ~int64_t{15}; }
 
 GradSpace grad_space(void* ws, int64_t vocab, int64_t dim, int64_t n_tokens, int64_t* bytes) {
     GradSpace g{};
-    g.lg = group_lg(vocab);
+    const bool sort = n_tokens > kFewTokens && vocab <= int64_t{kBuckets} * kBucketIds;
+    g.lg = kLgBuckets;
+    if (!sort)
+        while ((int64_t{kOwned} << g.lg) < vocab) ++g.lg;
     g.owned = static_cast<int>((vocab + (int64_t{1} << g.lg) - 1) >> g.lg);
     g.pieces = static_cast<int>((n_tokens + kPiece - 1) / kPiece);
     char* p = static_cast<char*>(ws);
@@ -96,61 +111,91 @@ GradSpace grad_space(void* ws, int64_t vocab, int64_t dim, int64_t n_tokens, int
     g.word = reinterpret_cast<int32_t*>(take(n_tokens + 1));
     g.count = reinterpret_cast<int32_t*>(take(static_cast<int64_t>(g.owned) << g.lg));
     g.part = reinterpret_cast<float*>(take(2 * g.pieces * ((dim + 3) & ~int64_t{3})));
+    if (sort) {
+        g.chunk_tokens = (n_tokens + kMostChunks - 1) / kMostChunks;
+        if (g.chunk_tokens < kChunkTokens) g.chunk_tokens = kChunkTokens;
+        g.chunk_tokens = (g.chunk_tokens + kSortThreads - 1) / kSortThreads * kSortThreads;
+        g.chunks = static_cast<int>((n_tokens + g.chunk_tokens - 1) / g.chunk_tokens);
+        g.hist = reinterpret_cast<int32_t*>(take(int64_t{g.chunks} * kBuckets));
+        g.start = reinterpret_cast<int32_t*>(take(kBuckets + 1));
+        g.bperm = reinterpret_cast<int32_t*>(take(n_tokens));
+        g.bword = reinterpret_cast<int32_t*>(take(n_tokens));
+    }
     if (bytes) *bytes = at;
     return g;
 }
 
+// Exclusive prefix over the lanes of a wave; *sum: the total.
+__device__ __forceinline__ int wave_prefix(int c, int lane, int* sum) {
+    int incl = c;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int up = __shfl_up(incl, o);
+        if (lane >= o) incl += up;
+    }
+    *sum = __shfl(incl, 63);
+    return incl - c;
+}
+
+// The wave's lanes of `valid` that hold the same key (of `bits` bits) as this one.
+__device__ __forceinline__ unsigned long long same_key(unsigned long long valid, int key, int bits) {
+    unsigned long long m = valid;
+    for (int b = 0; b < bits; ++b) {
+        const unsigned long long ones = __ballot((key >> b) & 1);
+        m &= (key >> b) & 1 ? ones : ~ones;
+    }
+    return m;
+}
+
 __global__ void __launch_bounds__(kThreads)
     group_kernel(const int32_t* __restrict__ tokens, int64_t n_tokens, int64_t vocab, GradSpace g) {
+    constexpr int kTake = 8;  // ids per lane in flight
     __shared__ int cnt[kThreads / 64][kOwned];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t p = static_cast<int64_t>(blockIdx.x) * (kThreads / 64) + wave;
     int* own = cnt[wave];
     const int64_t mask = (int64_t{1} << g.lg) - 1;
     const unsigned long long below = (1ull << lane) - 1;
+    const auto each = [&](auto&& f) {  // all ids in order, 64 at a time
+        for (int64_t b = 0; b < n_tokens; b += 64 * kTake) {
+            int32_t t[kTake];
+#pragma unroll
+            for (int q = 0; q < kTake; ++q) {
+                const int64_t n = b + q * 64 + lane;
+                t[q] = n < n_tokens ? tokens[n] : -1;
+            }
+#pragma unroll
+            for (int q = 0; q < kTake; ++q) f(b + q * 64 + lane, t[q]);
+        }
+    };
     for (int j = lane; j < g.owned; j += 64) own[j] = 0;
     __builtin_amdgcn_wave_barrier();
     int less = 0;
-    for (int64_t b = 0; b < n_tokens; b += 64) {
-        const int64_t n = b + lane;
-        const int32_t t = n < n_tokens ? tokens[n] : -1;
+    each([&](int64_t, int32_t t) {
         const bool ok = t >= 0 && t < vocab;
         less += __popcll(__ballot(ok && (t & mask) < p));
-        unsigned long long m = __ballot(ok && (t & mask) == p);
-        const int id = t >> g.lg;
-        while (m) {
-            const int x = __shfl(id, __builtin_ctzll(m));
-            const unsigned long long same = __ballot(id == x) & m;
-            if (lane == 0) own[x] += __popcll(same);
-            m &= ~same;
-        }
-    }
+        if (ok && (t & mask) == p) atomicAdd(&own[t >> g.lg], 1);
+    });
     __builtin_amdgcn_wave_barrier();
     int sum = less;  // exclusive prefix over the owned ids, after the ids of the waves before
     for (int j0 = 0; j0 < g.owned; j0 += 64) {
         const int j = j0 + lane;
         const int c = j < g.owned ? own[j] : 0;
-        int incl = c;
-        for (int o = 1; o < 64; o <<= 1) {
-            const int up = __shfl_up(incl, o);
-            if (lane >= o) incl += up;
-        }
+        int all;
+        const int before = wave_prefix(c, lane, &all);
         if (j < g.owned) {
             g.count[p * g.owned + j] = c;
-            own[j] = sum + incl - c;
+            own[j] = sum + before;
         }
-        sum += __shfl(incl, 63);
+        sum += all;
     }
     __builtin_amdgcn_wave_barrier();
     if (p == mask && lane == 0) {
         *g.total = sum;
         g.word[sum] = -1;
     }
-    for (int64_t b = 0; b < n_tokens; b += 64) {
-        const int64_t n = b + lane;
-        const int32_t t = n < n_tokens ? tokens[n] : -1;
-        const bool ok = t >= 0 && t < vocab;
-        unsigned long long m = __ballot(ok && (t & mask) == p);
+    each([&](int64_t n, int32_t t) {
+        unsigned long long m = __ballot(t >= 0 && t < vocab && (t & mask) == p);
         const int id = t >> g.lg;
         while (m) {
             const int x = __shfl(id, __builtin_ctzll(m));
@@ -166,7 +211,160 @@ __global__ void __launch_bounds__(kThreads)
             __builtin_amdgcn_wave_barrier();
             m &= ~same;
         }
+    });
+}
+
+// Positions of each residue in each chunk.
+__global__ void __launch_bounds__(kSortThreads)
+    bucket_count_kernel(const int32_t* __restrict__ tokens, int64_t n_tokens, int64_t vocab, GradSpace g) {
+    __shared__ int hist[kBuckets];
+    hist[threadIdx.x] = 0;
+    __syncthreads();
+    const int64_t n0 = blockIdx.x * g.chunk_tokens;
+    const int64_t n1 = n0 + g.chunk_tokens < n_tokens ? n0 + g.chunk_tokens : n_tokens;
+    for (int64_t n = n0 + threadIdx.x; n < n1; n += kSortThreads) {
+        const int32_t t = tokens[n];
+        if (t >= 0 && t < vocab) atomicAdd(&hist[t & (kBuckets - 1)], 1);
     }
+    __syncthreads();
+    g.hist[static_cast<int64_t>(blockIdx.x) * kBuckets + threadIdx.x] = hist[threadIdx.x];
+}
+
+// A chunk's positions into their buckets, in order: each wave counts its part
+// of the chunk, the counts of all waves and chunks before give each wave its
+// places, and equal residues within 64 positions follow one another by lane.
+__global__ void __launch_bounds__(kSortThreads)
+    bucket_scatter_kernel(const int32_t* __restrict__ tokens, int64_t n_tokens, int64_t vocab, GradSpace g) {
+    constexpr int kW = kSortThreads / 64;
+    static_assert(kSortThreads == kBuckets, "a thread per bucket");
+    __shared__ int place[kW][kBuckets];
+    __shared__ int sums[kW];
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    for (int w = 0; w < kW; ++w) place[w][t] = 0;
+    int before = 0, all = 0;  // positions of bucket t in the chunks before, in all chunks
+    for (int c = 0; c < g.chunks; ++c) {
+        const int h = g.hist[static_cast<int64_t>(c) * kBuckets + t];
+        before += c < static_cast<int>(blockIdx.x) ? h : 0;
+        all += h;
+    }
+    __syncthreads();
+    const int64_t part = g.chunk_tokens / kW;
+    const int64_t n0 = blockIdx.x * g.chunk_tokens + wave * part;
+    const int64_t n1 = n0 + part < n_tokens ? n0 + part : n_tokens;
+    for (int64_t n = n0 + lane; n < n1; n += 64) {
+        const int32_t x = tokens[n];
+        if (x >= 0 && x < vocab) atomicAdd(&place[wave][x & (kBuckets - 1)], 1);
+    }
+    int sum;
+    int start = wave_prefix(all, lane, &sum);
+    if (lane == 0) sums[wave] = sum;
+    __syncthreads();
+    for (int w = 0; w < wave; ++w) start += sums[w];
+    if (blockIdx.x == 0) {
+        g.start[t] = start;
+        if (t == kBuckets - 1) {
+            g.start[kBuckets] = start + all;
+            *g.total = start + all;
+            g.word[start + all] = -1;
+        }
+    }
+    int at = start + before;
+#pragma unroll
+    for (int w = 0; w < kW; ++w) {
+        const int c = place[w][t];
+        place[w][t] = at;
+        at += c;
+    }
+    __syncthreads();
+    for (int64_t b = n0; b < n1; b += 64) {
+        const int64_t n = b + lane;
+        const int32_t x = n < n1 ? tokens[n] : -1;
+        const bool ok = x >= 0 && x < vocab;
+        const int key = x & (kBuckets - 1);
+        const unsigned long long same = same_key(__ballot(ok), key, kLgBuckets);
+        const int first = ok ? place[wave][key] : 0;
+        __builtin_amdgcn_wave_barrier();
+        if (ok) {
+            const int to = first + __popcll(same & ((1ull << lane) - 1));
+            g.bperm[to] = static_cast<int32_t>(n);
+            g.bword[to] = x;
+            if (same >> lane == 1) place[wave][key] = to + 1;  // the last of its residue
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+// One bucket's positions grouped by id, in order, the same way.
+__global__ void __launch_bounds__(kThreads) bucket_group_kernel(GradSpace g, int id_bits) {
+    constexpr int kW = kThreads / 64;
+    __shared__ int place[kW][kBucketIds];
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    const int bucket = blockIdx.x;
+    const int i0 = g.start[bucket], n = g.start[bucket + 1] - i0;
+    for (int w = 0; w < kW; ++w)
+        for (int j = t; j < g.owned; j += kThreads) place[w][j] = 0;
+    __syncthreads();
+    const int part = ((n + kW - 1) / kW + 63) & ~63;
+    const int a = wave * part < n ? wave * part : n, b = a + part < n ? a + part : n;
+    for (int i = a + lane; i < b; i += 64) atomicAdd(&place[wave][g.bword[i0 + i] >> kLgBuckets], 1);
+    __syncthreads();
+    if (wave == 0) {
+        int sum = i0;
+        for (int j0 = 0; j0 < g.owned; j0 += 64) {
+            const int j = j0 + lane;
+            int c[kW], all = 0, total;
+#pragma unroll
+            for (int w = 0; w < kW; ++w) {
+                c[w] = j < g.owned ? place[w][j] : 0;
+                all += c[w];
+            }
+            int at = sum + wave_prefix(all, lane, &total);
+            if (j < g.owned) {
+                g.count[bucket * g.owned + j] = all;
+#pragma unroll
+                for (int w = 0; w < kW; ++w) {
+                    place[w][j] = at;
+                    at += c[w];
+                }
+            }
+            sum += total;
+        }
+    }
+    __syncthreads();
+    for (int i = a; i < b; i += 64) {
+        const bool ok = i + lane < b;
+        const int x = ok ? g.bword[i0 + i + lane] : 0;
+        const int key = x >> kLgBuckets;
+        const unsigned long long same = same_key(__ballot(ok), key, id_bits);
+        const int first = ok ? place[wave][key] : 0;
+        __builtin_amdgcn_wave_barrier();
+        if (ok) {
+            const int to = first + __popcll(same & ((1ull << lane) - 1));
+            g.perm[to] = g.bperm[i0 + i + lane];
+            g.word[to] = x;
+            if (same >> lane == 1) place[wave][key] = to + 1;
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+hipError_t launch_group(const EmbedGradArgs& a, const GradSpace& g, hipStream_t s) {
+    if (g.chunks == 0) {
+        group_kernel<<<dim3(static_cast<unsigned>((int64_t{1} << g.lg) / (kThreads / 64))), kThreads, 0, s>>>(
+            a.tokens, a.n_tokens, a.vocab, g);
+        return hipGetLastError();
+    }
+    const dim3 chunks(static_cast<unsigned>(g.chunks));
+    bucket_count_kernel<<<chunks, kSortThreads, 0, s>>>(a.tokens, a.n_tokens, a.vocab, g);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    bucket_scatter_kernel<<<chunks, kSortThreads, 0, s>>>(a.tokens, a.n_tokens, a.vocab, g);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    int id_bits = 0;
+    while ((1 << id_bits) < g.owned) ++id_bits;
+    bucket_group_kernel<<<dim3(kBuckets), kThreads, 0, s>>>(g, id_bits);
+    return hipGetLastError();
 }
 
 // V consecutive elements as one load or store (V * sizeof(E) is 2 to 16 bytes).
@@ -272,27 +470,44 @@ __global__ void __launch_bounds__(kThreads) run_sum_kernel(GradIn<EG, EO> a, Gra
     }
 }
 
-// Runs that leave the piece they begin in: their parts added in order, in
-// float64.
+// Runs that leave the piece they begin in: their parts added in float64, each
+// of the workgroup's waves a share of them in order, then the shares.
 template <class EG, class EO, int V>
 __global__ void __launch_bounds__(kThreads) run_join_kernel(GradIn<EG, EO> a, GradSpace g, Cover c) {
-    const Place at = place_of<V>(c);
-    const int64_t piece = at.unit, col = at.col;
+    constexpr int kW = kThreads / 64;
+    __shared__ double shares[kW][64][V];
+    const int64_t block = c.first + blockIdx.x;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t piece = block / c.tiles, col = (block % c.tiles * 64 + lane) * V;
     const int64_t total = *g.total, i0 = piece * kPiece, i1 = i0 + kPiece;
-    if (i1 >= total || col >= a.dim) return;
+    if (i1 >= total) return;
     const int32_t word = g.word[i1 - 1];
-    if (g.word[i1] != word) return;                                     // no run leaves this piece
+    if (g.word[i1] != word) return;                                      // no run leaves this piece
     if (g.word[i0] == word && i0 > 0 && g.word[i0 - 1] == word) return;  // it began before
+    const bool in_run = lane < kPiece && g.word[i0 + lane] == word;  // the piece's last positions
+    const int64_t begin = i1 - __popcll(__ballot(in_run));
+    const int64_t mask = (int64_t{1} << g.lg) - 1;
+    const int64_t end = begin + g.count[(word & mask) * g.owned + (word >> g.lg)];
     const int64_t wide = (a.dim + 3) & ~int64_t{3};
-    double sum[V];
-    const float* from = g.part + (piece * 2 + 1) * wide + col;
+    const int64_t last = (end - 1) / kPiece, per = (last - piece + kW) / kW;  // parts `piece` to `last`
+    const int64_t q0 = piece + wave * per, q1 = q0 + per < last + 1 ? q0 + per : last + 1;
+    double sum[V] = {};
+    if (col < a.dim) {
+#pragma unroll 8
+        for (int64_t q = q0; q < q1; ++q) {
+            const float* p = g.part + (q * 2 + (q == piece ? 1 : 0)) * wide + col;
 #pragma unroll
-    for (int e = 0; e < V; ++e) sum[e] = from[e];
-    for (int64_t q = piece + 1; q * kPiece < total && g.word[q * kPiece] == word; ++q) {
-        const float* p = g.part + q * 2 * wide + col;
-#pragma unroll
-        for (int e = 0; e < V; ++e) sum[e] += p[e];
+            for (int e = 0; e < V; ++e) sum[e] += p[e];
+        }
     }
+#pragma unroll
+    for (int e = 0; e < V; ++e) shares[wave][lane][e] = sum[e];
+    __syncthreads();
+    if (wave != 0 || col >= a.dim) return;
+#pragma unroll
+    for (int w = 1; w < kW; ++w)
+#pragma unroll
+        for (int e = 0; e < V; ++e) sum[e] += shares[w][lane][e];
     finish<EG, EO, V>(a, word, col, sum);
 }
 
@@ -316,7 +531,8 @@ hipError_t grad_vec(const EmbedGradArgs& a, const GradSpace& g, hipStream_t s) {
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    n = blocks_of(g.pieces - 1);
+    c.tiles = static_cast<int>((a.dim + 64 * V - 1) / (64 * V));
+    n = int64_t{g.pieces - 1} * c.tiles;
     for (c.first = 0; c.first < n; c.first += per) {
         run_join_kernel<EG, EO, V><<<dim3(static_cast<unsigned>(n - c.first < per ? n - c.first : per)), kThreads, 0, s>>>(
             in, g, c);
@@ -328,9 +544,7 @@ hipError_t grad_vec(const EmbedGradArgs& a, const GradSpace& g, hipStream_t s) {
 
 template <class EG, class EO>
 hipError_t grad_typed(const EmbedGradArgs& a, const GradSpace& g, hipStream_t s) {
-    group_kernel<<<dim3(static_cast<unsigned>((int64_t{1} << g.lg) / (kThreads / 64))), kThreads, 0, s>>>(
-        a.tokens, a.n_tokens, a.vocab, g);
-    const hipError_t e = hipGetLastError();
+    const hipError_t e = launch_group(a, g, s);
     if (e != hipSuccess) return e;
     // widest access that both arrays' rows allow, 16 bytes of the wider type
     constexpr int kMost = sizeof(EG) + sizeof(EO) == 4 ? 8 : 4;
