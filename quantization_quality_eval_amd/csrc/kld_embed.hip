@@ -11,7 +11,7 @@
 //      id, counts its own and the ones of the waves before it, and writes its
 //      positions; no wave waits for another. More: a counting sort by v mod P
 //      first (count, scatter), after which a workgroup sorts one residue's.
-//   2. sum: the sorted order is cut into pieces of kPiece positions; a workgroup
+//   2. sum: the sorted order is cut into pieces of 8 to 32 positions; a workgroup
 //      adds up the runs of one piece for one tile of columns. A run that lies
 //      in the piece is done; of a run that reaches past it the piece's part is
 //      kept in float32. Further workgroups of the launch set the rows that no
@@ -58,17 +58,20 @@ __global__ void __launch_bounds__(kThreads)
 
 // ---- gradient ----
 
-constexpr int kPiece = 32;    // positions per workgroup of the sum
+constexpr int kMostPiece = 32;   // positions per piece of the sum: this many where there are
+constexpr int kLeastPiece = 8;   // waves enough, down to this many where there are not
+constexpr int64_t kPieceWaves = 4096;
 constexpr int kAhead = 8;     // rows in flight per thread
-static_assert(kPiece <= 64, "a lane per position");
+constexpr int kZeroRows = 8;  // rows of the table that a thread zeroes
+static_assert(kMostPiece < 64, "a lane per position and one more");
 
 // The counting sort of many positions.
 constexpr int kLgBuckets = 10;
 constexpr int kBuckets = 1 << kLgBuckets;
 constexpr int kBucketIds = 1024;      // ids of one bucket at most
 constexpr int kSortThreads = 1024;
-constexpr int kMostChunks = 64;       // workgroups of its first two launches
-constexpr int64_t kChunkTokens = 2048;  // positions of one of them at least
+constexpr int kMostChunks = 32;       // workgroups of its first two launches
+constexpr int64_t kChunkTokens = 1024;  // positions of one of them at least
 constexpr int64_t kFewTokens = 2048;    // up to here every wave reads every id
 
 struct GradSpace {
@@ -79,6 +82,7 @@ struct GradSpace {
     float* part;       // [pieces][2][dim]: a piece's part of the run that enters it, of the run that leaves it
     int lg;            // log2 P
     int owned;         // ids per residue
+    int piece;         // positions per piece
     int pieces;
     // counting sort only (chunks > 0)
     int chunks;
@@ -98,7 +102,9 @@ GradSpace grad_space(void* ws, int64_t vocab, int64_t dim, int64_t n_tokens, int
     if (!sort)
         while ((int64_t{kOwned} << g.lg) < vocab) ++g.lg;
     g.owned = static_cast<int>((vocab + (int64_t{1} << g.lg) - 1) >> g.lg);
-    g.pieces = static_cast<int>((n_tokens + kPiece - 1) / kPiece);
+    g.piece = kMostPiece;
+    while (g.piece > kLeastPiece && n_tokens / g.piece * ((dim + 255) / 256) < kPieceWaves) g.piece /= 2;
+    g.pieces = static_cast<int>((n_tokens + g.piece - 1) / g.piece);
     char* p = static_cast<char*>(ws);
     int64_t at = 0;
     const auto take = [&](int64_t n) {
@@ -242,6 +248,7 @@ __global__ void __launch_bounds__(kSortThreads)
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     for (int w = 0; w < kW; ++w) place[w][t] = 0;
     int before = 0, all = 0;  // positions of bucket t in the chunks before, in all chunks
+#pragma unroll 8
     for (int c = 0; c < g.chunks; ++c) {
         const int h = g.hist[static_cast<int64_t>(c) * kBuckets + t];
         before += c < static_cast<int>(blockIdx.x) ? h : 0;
@@ -409,7 +416,6 @@ struct Cover {
     int64_t first;
     int lanes;
     int tiles;
-    int zero_rows;
 };
 struct Place {
     int64_t unit;
@@ -424,42 +430,56 @@ __device__ __forceinline__ Place place_of(const Cover& c) {
 template <class EG, class EO, int V>
 __global__ void __launch_bounds__(kThreads) run_sum_kernel(GradIn<EG, EO> a, GradSpace g, Cover c) {
     const Place at = place_of<V>(c);
-    const int64_t piece = at.unit, col = at.col;
-    if (col >= a.dim) return;
+    const int piece = __builtin_amdgcn_readfirstlane(static_cast<int>(at.unit));  // one per wave
+    const int64_t col = at.col;
+    const int lane = threadIdx.x & 63;
     if (piece >= g.pieces) {
-        if (a.accumulate) return;  // the last workgroup may reach past the pieces
+        if (a.accumulate || col >= a.dim) return;  // the last workgroup may reach past the pieces
         const int64_t mask = (int64_t{1} << g.lg) - 1;
-        const int64_t v0 = (piece - g.pieces) * c.zero_rows;
-        const int64_t v1 = v0 + c.zero_rows < a.vocab ? v0 + c.zero_rows : a.vocab;
-        for (int64_t v = v0; v < v1; ++v)
-            if (g.count[(v & mask) * g.owned + (v >> g.lg)] == 0)
-                *reinterpret_cast<Vec<EO, V>*>(a.out + v * a.out_stride + col) = Vec<EO, V>{};
+        const int64_t v0 = (at.unit - g.pieces) * kZeroRows;
+        int named[kZeroRows];
+#pragma unroll
+        for (int q = 0; q < kZeroRows; ++q) {
+            const int64_t v = v0 + q;
+            named[q] = v < a.vocab ? g.count[(v & mask) * g.owned + (v >> g.lg)] : 1;
+        }
+#pragma unroll
+        for (int q = 0; q < kZeroRows; ++q)
+            if (named[q] == 0) *reinterpret_cast<Vec<EO, V>*>(a.out + (v0 + q) * a.out_stride + col) = Vec<EO, V>{};
         return;
     }
+    // lane l holds the piece's l-th position and its id; lane n the id behind the piece
     const int total = *g.total;
-    const int i0 = static_cast<int>(piece) * kPiece;
+    const int i0 = piece * g.piece;
     if (i0 >= total) return;
-    const int i1 = i0 + kPiece < total ? i0 + kPiece : total;
+    const int n = i0 + g.piece < total ? g.piece : total - i0;
+    const int words = lane <= n ? g.word[i0 + lane] : -1;
+    const int perms = lane < n ? g.perm[i0 + lane] : 0;
+    bool entered = i0 > 0 && g.word[i0 - 1] == __builtin_amdgcn_readlane(words, 0);
+    if (col >= a.dim) return;
     const int64_t wide = (a.dim + 3) & ~int64_t{3};
-    bool entered = i0 > 0 && g.word[i0 - 1] == g.word[i0];
+    const EG* from = a.grad + col;
     float acc[V] = {};
-    for (int i = i0; i < i1; i += kAhead) {
+#pragma unroll 1
+    for (int i = 0; i < n; i += kAhead) {
         Vec<EG, V> row[kAhead];
 #pragma unroll
         for (int q = 0; q < kAhead; ++q)
-            if (i + q < i1) row[q] = *reinterpret_cast<const Vec<EG, V>*>(a.grad + g.perm[i + q] * a.grad_stride + col);
+            if (i + q < n)
+                row[q] = *reinterpret_cast<const Vec<EG, V>*>(
+                    from + __builtin_amdgcn_readlane(perms, i + q) * a.grad_stride);
 #pragma unroll
         for (int q = 0; q < kAhead; ++q) {
-            if (i + q >= i1) break;
+            if (i + q >= n) break;
 #pragma unroll
             for (int e = 0; e < V; ++e) acc[e] += widen(row[q].x[e]);
-            const int32_t word = g.word[i + q];
-            const bool ends = g.word[i + q + 1] != word;
-            if (!ends && i + q + 1 < i1) continue;
+            const int word = __builtin_amdgcn_readlane(words, i + q);
+            const bool ends = __builtin_amdgcn_readlane(words, i + q + 1) != word;
+            if (!ends && i + q + 1 < n) continue;
             if (ends && !entered) {
                 finish<EG, EO, V>(a, word, col, acc);
             } else {
-                float* to = g.part + (piece * 2 + (entered ? 0 : 1)) * wide + col;
+                float* to = g.part + (int64_t{piece} * 2 + (entered ? 0 : 1)) * wide + col;
 #pragma unroll
                 for (int e = 0; e < V; ++e) to[e] = acc[e];
             }
@@ -479,17 +499,17 @@ __global__ void __launch_bounds__(kThreads) run_join_kernel(GradIn<EG, EO> a, Gr
     const int64_t block = c.first + blockIdx.x;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t piece = block / c.tiles, col = (block % c.tiles * 64 + lane) * V;
-    const int64_t total = *g.total, i0 = piece * kPiece, i1 = i0 + kPiece;
+    const int64_t total = *g.total, i0 = piece * g.piece, i1 = i0 + g.piece;
     if (i1 >= total) return;
     const int32_t word = g.word[i1 - 1];
     if (g.word[i1] != word) return;                                      // no run leaves this piece
     if (g.word[i0] == word && i0 > 0 && g.word[i0 - 1] == word) return;  // it began before
-    const bool in_run = lane < kPiece && g.word[i0 + lane] == word;  // the piece's last positions
+    const bool in_run = lane < g.piece && g.word[i0 + lane] == word;  // the piece's last positions
     const int64_t begin = i1 - __popcll(__ballot(in_run));
     const int64_t mask = (int64_t{1} << g.lg) - 1;
     const int64_t end = begin + g.count[(word & mask) * g.owned + (word >> g.lg)];
     const int64_t wide = (a.dim + 3) & ~int64_t{3};
-    const int64_t last = (end - 1) / kPiece, per = (last - piece + kW) / kW;  // parts `piece` to `last`
+    const int64_t last = (end - 1) / g.piece, per = (last - piece + kW) / kW;  // parts `piece` to `last`
     const int64_t q0 = piece + wave * per, q1 = q0 + per < last + 1 ? q0 + per : last + 1;
     double sum[V] = {};
     if (col < a.dim) {
@@ -515,10 +535,10 @@ template <class EG, class EO, int V>
 hipError_t grad_vec(const EmbedGradArgs& a, const GradSpace& g, hipStream_t s) {
     const GradIn<EG, EO> in{static_cast<const EG*>(a.grad), a.grad_stride, a.dim,   a.scale,
                             static_cast<EO*>(a.out),        a.out_stride,  a.vocab, a.accumulate};
-    Cover c{0, 64, 1, 8};
+    Cover c{0, 64, 1};
     while (c.lanes < kThreads && int64_t{c.lanes} * V < a.dim) c.lanes *= 2;
     c.tiles = static_cast<int>((a.dim + int64_t{c.lanes} * V - 1) / (int64_t{c.lanes} * V));
-    const int64_t zero_units = a.accumulate ? 0 : (a.vocab + c.zero_rows - 1) / c.zero_rows;
+    const int64_t zero_units = a.accumulate ? 0 : (a.vocab + kZeroRows - 1) / kZeroRows;
     const int64_t per = max_blocks_per_launch(kThreads);
     const auto blocks_of = [&](int64_t units) {
         const int64_t in_block = kThreads / c.lanes;
