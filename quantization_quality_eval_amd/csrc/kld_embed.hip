@@ -21,6 +21,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "kld_vocab.h"
 
 namespace kldk {
@@ -41,19 +43,81 @@ __device__ __forceinline__ uint16_t to_bf16(float x) {
 __device__ __forceinline__ void put(float* p, float x) { *p = x; }
 __device__ __forceinline__ void put(uint16_t* p, float x) { *p = to_bf16(x); }
 
-template <class ET, class EO>
+// V consecutive elements as one load or store (V * sizeof(E) is 2 to 16 bytes).
+template <class E, int V>
+struct alignas(V * sizeof(E)) Vec {
+    E x[V];
+};
+
+// How a launch covers rows and columns: `lanes` threads (a power of two from 64
+// to kThreads) of V elements each take one tile of a row's columns, tile after
+// tile, row unit after row unit; `first`: the launch's first workgroup.
+struct Cover {
+    int64_t first;
+    int lanes;
+    int tiles;
+};
+struct Place {
+    int64_t unit;
+    int64_t col;
+};
+template <int V>
+__device__ __forceinline__ Place place_of(const Cover& c) {
+    const int64_t i = (c.first + blockIdx.x) * (kThreads / c.lanes) + threadIdx.x / c.lanes;
+    return Place{i / c.tiles, (i % c.tiles * c.lanes + threadIdx.x % c.lanes) * V};
+}
+
+template <int V>
+Cover cover_of(int64_t dim) {
+    Cover c{0, 64, 1};
+    while (c.lanes < kThreads && int64_t{c.lanes} * V < dim) c.lanes *= 2;
+    c.tiles = static_cast<int>((dim + int64_t{c.lanes} * V - 1) / (int64_t{c.lanes} * V));
+    return c;
+}
+
+// Launch f(c, blocks) until `units` row units are covered.
+template <class F>
+hipError_t launch_cover(Cover c, int64_t units, F&& f) {
+    const int64_t in_block = kThreads / c.lanes, per = max_blocks_per_launch(kThreads);
+    const int64_t n = (units * c.tiles + in_block - 1) / in_block;
+    for (; c.first < n; c.first += per) {
+        f(c, dim3(static_cast<unsigned>(n - c.first < per ? n - c.first : per)));
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+// Whether rows of `dim` elements can be accessed V elements at a time.
+bool allows(int v, int64_t dim, const void* p, int64_t stride, size_t size) {
+    return dim % v == 0 && stride % v == 0 && reinterpret_cast<uintptr_t>(p) % (v * size) == 0;
+}
+// Elements of 16 bytes of the wider type.
+template <class A, class B>
+constexpr int widest() {
+    return sizeof(A) + sizeof(B) == 4 ? 8 : 4;
+}
+
+// ---- lookup ----
+
+template <class ET, class EO, int V>
 __global__ void __launch_bounds__(kThreads)
     embed_kernel(const ET* __restrict__ table, int64_t vocab, int64_t dim, int64_t table_stride,
-                 const int32_t* __restrict__ tokens, double scale, EO* __restrict__ out, int64_t out_stride) {
-    const int64_t n = blockIdx.x;
-    const int32_t t = tokens[n];
-    EO* o = out + n * out_stride;
-    for (int64_t c = threadIdx.x; c < dim; c += kThreads) {
-        float x = 0.0f;
-        if (t >= vocab) x = NAN;
-        else if (t >= 0) x = static_cast<float>(static_cast<double>(widen(table[t * table_stride + c])) * scale);
-        put(o + c, x);
+                 const int32_t* __restrict__ tokens, int64_t n_tokens, double scale, EO* __restrict__ out,
+                 int64_t out_stride, Cover c) {
+    const Place at = place_of<V>(c);
+    if (at.unit >= n_tokens || at.col >= dim) return;
+    const int32_t t = tokens[at.unit];
+    Vec<EO, V> o;
+    if (t >= 0 && t < vocab) {
+        const Vec<ET, V> x = *reinterpret_cast<const Vec<ET, V>*>(table + t * table_stride + at.col);
+#pragma unroll
+        for (int e = 0; e < V; ++e) put(&o.x[e], static_cast<float>(static_cast<double>(widen(x.x[e])) * scale));
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) put(&o.x[e], t < 0 ? 0.0f : NAN);
     }
+    *reinterpret_cast<Vec<EO, V>*>(out + at.unit * out_stride + at.col) = o;
 }
 
 // ---- gradient ----
@@ -374,12 +438,6 @@ hipError_t launch_group(const EmbedGradArgs& a, const GradSpace& g, hipStream_t 
     return hipGetLastError();
 }
 
-// V consecutive elements as one load or store (V * sizeof(E) is 2 to 16 bytes).
-template <class E, int V>
-struct alignas(V * sizeof(E)) Vec {
-    E x[V];
-};
-
 template <class EG, class EO>
 struct GradIn {
     const EG* grad;
@@ -406,25 +464,6 @@ __device__ __forceinline__ void finish(const GradIn<EG, EO>& a, int32_t word, in
         put(&v.x[e], static_cast<float>(s));
     }
     *o = v;
-}
-
-// How a launch covers rows and columns: `lanes` threads (a power of two from 64
-// to kThreads) of V elements each take one tile of a row's columns, tile after
-// tile, row unit after row unit (pieces of the sorted order, then groups of
-// rows to zero); `first`: the launch's first workgroup.
-struct Cover {
-    int64_t first;
-    int lanes;
-    int tiles;
-};
-struct Place {
-    int64_t unit;
-    int64_t col;
-};
-template <int V>
-__device__ __forceinline__ Place place_of(const Cover& c) {
-    const int64_t i = (c.first + blockIdx.x) * (kThreads / c.lanes) + threadIdx.x / c.lanes;
-    return Place{i / c.tiles, (i % c.tiles * c.lanes + threadIdx.x % c.lanes) * V};
 }
 
 template <class EG, class EO, int V>
@@ -535,62 +574,49 @@ template <class EG, class EO, int V>
 hipError_t grad_vec(const EmbedGradArgs& a, const GradSpace& g, hipStream_t s) {
     const GradIn<EG, EO> in{static_cast<const EG*>(a.grad), a.grad_stride, a.dim,   a.scale,
                             static_cast<EO*>(a.out),        a.out_stride,  a.vocab, a.accumulate};
-    Cover c{0, 64, 1};
-    while (c.lanes < kThreads && int64_t{c.lanes} * V < a.dim) c.lanes *= 2;
-    c.tiles = static_cast<int>((a.dim + int64_t{c.lanes} * V - 1) / (int64_t{c.lanes} * V));
     const int64_t zero_units = a.accumulate ? 0 : (a.vocab + kZeroRows - 1) / kZeroRows;
-    const int64_t per = max_blocks_per_launch(kThreads);
-    const auto blocks_of = [&](int64_t units) {
-        const int64_t in_block = kThreads / c.lanes;
-        return (units * c.tiles + in_block - 1) / in_block;
-    };
-    int64_t n = blocks_of(g.pieces + zero_units);
-    for (c.first = 0; c.first < n; c.first += per) {
-        run_sum_kernel<EG, EO, V><<<dim3(static_cast<unsigned>(n - c.first < per ? n - c.first : per)), kThreads, 0, s>>>(
-            in, g, c);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
-    c.tiles = static_cast<int>((a.dim + 64 * V - 1) / (64 * V));
-    n = int64_t{g.pieces - 1} * c.tiles;
-    for (c.first = 0; c.first < n; c.first += per) {
-        run_join_kernel<EG, EO, V><<<dim3(static_cast<unsigned>(n - c.first < per ? n - c.first : per)), kThreads, 0, s>>>(
-            in, g, c);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
-    return hipSuccess;
+    const hipError_t e = launch_cover(cover_of<V>(a.dim), g.pieces + zero_units, [&](const Cover& c, dim3 blocks) {
+        run_sum_kernel<EG, EO, V><<<blocks, kThreads, 0, s>>>(in, g, c);
+    });
+    if (e != hipSuccess || g.pieces < 2) return e;
+    // a whole workgroup per unit of 64 V columns
+    const Cover join{0, kThreads, static_cast<int>((a.dim + 64 * V - 1) / (64 * V))};
+    return launch_cover(join, g.pieces - 1, [&](const Cover& c, dim3 blocks) {
+        run_join_kernel<EG, EO, V><<<blocks, kThreads, 0, s>>>(in, g, c);
+    });
 }
 
 template <class EG, class EO>
 hipError_t grad_typed(const EmbedGradArgs& a, const GradSpace& g, hipStream_t s) {
     const hipError_t e = launch_group(a, g, s);
     if (e != hipSuccess) return e;
-    // widest access that both arrays' rows allow, 16 bytes of the wider type
-    constexpr int kMost = sizeof(EG) + sizeof(EO) == 4 ? 8 : 4;
-    const auto allows = [&](int v) {
-        return a.dim % v == 0 && a.grad_stride % v == 0 && a.out_stride % v == 0 &&
-               reinterpret_cast<uintptr_t>(a.grad) % (v * sizeof(EG)) == 0 &&
-               reinterpret_cast<uintptr_t>(a.out) % (v * sizeof(EO)) == 0;
+    const auto both = [&](int v) {
+        return allows(v, a.dim, a.grad, a.grad_stride, sizeof(EG)) && allows(v, a.dim, a.out, a.out_stride, sizeof(EO));
     };
-    if (allows(kMost)) return grad_vec<EG, EO, kMost>(a, g, s);
-    if (allows(2)) return grad_vec<EG, EO, 2>(a, g, s);
+    constexpr int kMost = widest<EG, EO>();
+    if (both(kMost)) return grad_vec<EG, EO, kMost>(a, g, s);
+    if (both(2)) return grad_vec<EG, EO, 2>(a, g, s);
     return grad_vec<EG, EO, 1>(a, g, s);
 }
 
 template <class ET, class EO>
 hipError_t embed_typed(const void* table, int64_t vocab, int64_t dim, int64_t table_stride, const int32_t* tokens,
                        int64_t n_tokens, double scale, void* out, int64_t out_stride, hipStream_t s) {
-    const int64_t per = max_blocks_per_launch(kThreads);
-    for (int64_t done = 0; done < n_tokens; done += per) {
-        const int64_t n = n_tokens - done < per ? n_tokens - done : per;
-        embed_kernel<ET, EO><<<dim3(static_cast<unsigned>(n)), kThreads, 0, s>>>(
-            static_cast<const ET*>(table), vocab, dim, table_stride, tokens + done, scale,
-            static_cast<EO*>(out) + done * out_stride, out_stride);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
-    return hipSuccess;
+    const auto run = [&](auto v) {
+        constexpr int V = decltype(v)::value;
+        return launch_cover(cover_of<V>(dim), n_tokens, [&](const Cover& c, dim3 blocks) {
+            embed_kernel<ET, EO, V><<<blocks, kThreads, 0, s>>>(static_cast<const ET*>(table), vocab, dim, table_stride,
+                                                               tokens, n_tokens, scale, static_cast<EO*>(out),
+                                                               out_stride, c);
+        });
+    };
+    const auto both = [&](int v) {
+        return allows(v, dim, table, table_stride, sizeof(ET)) && allows(v, dim, out, out_stride, sizeof(EO));
+    };
+    constexpr int kMost = widest<ET, EO>();
+    if (both(kMost)) return run(std::integral_constant<int, kMost>{});
+    if (both(2)) return run(std::integral_constant<int, 2>{});
+    return run(std::integral_constant<int, 1>{});
 }
 
 }  // namespace

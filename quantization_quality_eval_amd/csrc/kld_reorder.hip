@@ -16,6 +16,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kStatesPerLaunch = 64;
+constexpr int64_t kMostChunks = 1024;  // workgroups along one item's positions
 
 struct StateList {
     char* p[kStatesPerLaunch];
@@ -23,86 +24,114 @@ struct StateList {
 
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 
+// One workgroup: a run of kThreads units per state, outer index and item, in
+// steps of the grid.
+struct Grid {
+    int64_t items;   // of this launch
+    int64_t chunks;  // workgroups along the positions
+};
+
 template <class U, int W>
 __global__ void __launch_bounds__(kThreads)
-    reorder_kernel(StateList list, int w_n, const int32_t* __restrict__ parents, int64_t beam_stride,
+    reorder_kernel(StateList list, int w_n, const int32_t* __restrict__ parents, int64_t beam_stride, int64_t n_outer,
                    int64_t outer_stride, int64_t n_positions, int64_t position_bytes,
-                   const int32_t* __restrict__ lengths) {
-    const int64_t item = blockIdx.y;
-    // blockIdx.z: state, blockIdx.x: outer x chunk, see the launcher
-    const int64_t chunks = gridDim.x;
+                   const int32_t* __restrict__ lengths, Grid g, int64_t first) {
+    int64_t i = first + blockIdx.x;
+    const int64_t chunk = i % g.chunks;
+    i /= g.chunks;
+    const int64_t outer = i % n_outer;
+    i /= n_outer;
+    const int64_t item = i % g.items;
+    const int state = static_cast<int>(i / g.items);
     int64_t n = n_positions;
     if (lengths) {
         const int64_t l = lengths[item];
         n = l < 0 ? 0 : l < n ? l : n;
     }
     const int64_t units = n * (position_bytes / static_cast<int64_t>(sizeof(U)));
+    if (chunk * kThreads >= units) return;
     const int32_t* pa = parents + item * w_n;
-    char* base = list.p[blockIdx.z % kStatesPerLaunch] + (blockIdx.z / kStatesPerLaunch) * outer_stride +
-                 item * w_n * beam_stride;
-    int src[W];
+    int64_t src[W];  // byte offset of the beam that moves here, -1: it stays
+    bool any = false;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-        src[w] = w;
+        src[w] = -1;
         if (w < w_n) {
             const int p = pa[w];
-            if (p >= 0 && p < w_n) src[w] = p;
+            if (p >= 0 && p < w_n && p != w) src[w] = p * beam_stride, any = true;
         }
     }
-    for (int64_t i = blockIdx.x * kThreads + threadIdx.x; i < units; i += chunks * kThreads) {
+    if (!any) return;
+    char* base = list.p[state] + outer * outer_stride + item * w_n * beam_stride;
+    for (int64_t u = chunk * kThreads + threadIdx.x; u < units; u += g.chunks * kThreads) {
+        char* at = base + u * static_cast<int64_t>(sizeof(U));
         U v[W];
 #pragma unroll
         for (int w = 0; w < W; ++w)
-            if (src[w] != w) v[w] = *reinterpret_cast<const U*>(base + src[w] * beam_stride + i * sizeof(U));
+            if (src[w] >= 0) v[w] = *reinterpret_cast<const U*>(at + src[w]);
 #pragma unroll
         for (int w = 0; w < W; ++w)
-            if (src[w] != w) *reinterpret_cast<U*>(base + w * beam_stride + i * sizeof(U)) = v[w];
+            if (src[w] >= 0) *reinterpret_cast<U*>(at + w * beam_stride) = v[w];
     }
 }
 
 template <class U, int W>
-hipError_t launch_shape(const ReorderArgs& a, int64_t item, int n_items, int state, int n_states, int64_t outer,
-                        hipStream_t s) {
-    StateList list{};
-    for (int k = 0; k < n_states; ++k)
-        list.p[k] = static_cast<char*>(a.states[state + k]) + outer * a.outer_stride + item * a.n_beams * a.beam_stride;
+hipError_t launch_shape(const ReorderArgs& a, hipStream_t s) {
     const int64_t units = a.n_positions * (a.position_bytes / static_cast<int64_t>(sizeof(U)));
-    int64_t x = (units + kThreads - 1) / kThreads;
-    if (x > 1024) x = 1024;
-    reorder_kernel<U, W><<<dim3(static_cast<unsigned>(x), static_cast<unsigned>(n_items),
-                                static_cast<unsigned>(n_states)), kThreads, 0, s>>>(
-        list, a.n_beams, a.parents + item * a.n_beams, a.beam_stride, a.outer_stride, a.n_positions, a.position_bytes,
-        a.lengths ? a.lengths + item : nullptr);
-    return hipGetLastError();
+    int64_t chunks = (units + kThreads - 1) / kThreads;
+    if (chunks > kMostChunks) chunks = kMostChunks;
+    const int64_t per = max_blocks_per_launch(kThreads);
+    for (int k = 0; k < a.n_states; k += kStatesPerLaunch) {
+        StateList list{};
+        const int ns = a.n_states - k < kStatesPerLaunch ? a.n_states - k : kStatesPerLaunch;
+        for (int q = 0; q < ns; ++q) list.p[q] = static_cast<char*>(a.states[k + q]);
+        const Grid g{a.n_items, chunks};
+        const int64_t blocks = chunks * a.n_outer * a.n_items * ns;
+        for (int64_t first = 0; first < blocks; first += per) {
+            const int64_t n = blocks - first < per ? blocks - first : per;
+            reorder_kernel<U, W><<<dim3(static_cast<unsigned>(n)), kThreads, 0, s>>>(
+                list, a.n_beams, a.parents, a.beam_stride, a.n_outer, a.outer_stride, a.n_positions, a.position_bytes,
+                a.lengths, g, first);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+        }
+    }
+    return hipSuccess;
 }
 
+// The registers that hold an item's units bound the unit: 64 beams of 4 bytes,
+// 16 of 16.
 template <class U>
-hipError_t launch_beams(const ReorderArgs& a, int64_t item, int n_items, int state, int n_states, int64_t outer,
-                        hipStream_t s) {
-    if (a.n_beams <= 4) return launch_shape<U, 4>(a, item, n_items, state, n_states, outer, s);
-    if (a.n_beams <= 16) return launch_shape<U, 16>(a, item, n_items, state, n_states, outer, s);
-    return launch_shape<U, 64>(a, item, n_items, state, n_states, outer, s);
+hipError_t launch_beams(const ReorderArgs& a, hipStream_t s) {
+    if (a.n_beams <= 4) return launch_shape<U, 4>(a, s);
+    if (a.n_beams <= 8) return launch_shape<U, 8>(a, s);
+    if constexpr (sizeof(U) <= 16)
+        if (a.n_beams <= 16) return launch_shape<U, 16>(a, s);
+    if constexpr (sizeof(U) <= 8)
+        if (a.n_beams <= 32) return launch_shape<U, 32>(a, s);
+    if constexpr (sizeof(U) <= 4) return launch_shape<U, 64>(a, s);
+    return hipErrorInvalidValue;
 }
 
 }  // namespace
 
 hipError_t launch_beam_reorder(const ReorderArgs& a, hipStream_t stream) {
-    uint64_t bits = static_cast<uint64_t>(a.position_bytes);
+    uint64_t bits = 0;  // everything that a unit has to divide
     if (a.n_items * a.n_beams > 1) bits |= static_cast<uint64_t>(a.beam_stride);
     if (a.n_outer > 1) bits |= static_cast<uint64_t>(a.outer_stride);
     for (int k = 0; k < a.n_states; ++k) bits |= reinterpret_cast<uintptr_t>(a.states[k]);
-    for (int k = 0; k < a.n_states; k += kStatesPerLaunch)
-        for (int64_t o = 0; o < a.n_outer; ++o)
-            for (int64_t b = 0; b < a.n_items; b += 32768) {
-                const int ns = a.n_states - k < kStatesPerLaunch ? a.n_states - k : kStatesPerLaunch;
-                const int nb = static_cast<int>(a.n_items - b < 32768 ? a.n_items - b : 32768);
-                hipError_t e;
-                if (bits % 4 == 0) e = launch_beams<uint32_t>(a, b, nb, k, ns, o, stream);
-                else if (bits % 2 == 0) e = launch_beams<uint16_t>(a, b, nb, k, ns, o, stream);
-                else e = launch_beams<uint8_t>(a, b, nb, k, ns, o, stream);
-                if (e != hipSuccess) return e;
-            }
-    return hipSuccess;
+    // without lengths a beam's positions are one run of bytes
+    ReorderArgs whole = a;
+    if (!a.lengths) {
+        whole.position_bytes = a.n_positions * a.position_bytes;
+        whole.n_positions = 1;
+    }
+    bits |= static_cast<uint64_t>(whole.position_bytes);
+    if (bits % 16 == 0 && a.n_beams <= 16) return launch_beams<u32x4>(whole, stream);
+    if (bits % 8 == 0 && a.n_beams <= 32) return launch_beams<uint64_t>(whole, stream);
+    if (bits % 4 == 0) return launch_beams<uint32_t>(whole, stream);
+    if (bits % 2 == 0) return launch_beams<uint16_t>(whole, stream);
+    return launch_beams<uint8_t>(whole, stream);
 }
 
 }  // namespace kldk
