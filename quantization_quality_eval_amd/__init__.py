@@ -19,6 +19,7 @@ calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -656,49 +657,67 @@ def compare_tokens(base, quant, tokens, stream=None, allow_invalid: bool = False
 
 # ---- operators around the model's vocabulary (no handle) ----
 
+# These calls are made once per token of a decoding loop, so what they do on the
+# host is kept short: one test per tensor on the path without errors, sizes of
+# workspaces remembered by their arguments.
+
 def _device_of(t, name):
     if not t.is_cuda:
         raise ValueError(f"{name}: expected a device tensor, got one on {t.device}")
     return t.device
 
 
-class _Launch:
-    """The device a call works on, made current for the call, and its stream.
-    What the call allocates belongs to that stream: memory that other streams
-    let go of may still be in use there."""
-
-    def __init__(self, device, stream):
+def _raw_stream(stream, device) -> int:
+    if stream is None:
         import torch
-        if stream is not None and stream.device != device:
-            raise ValueError(f"stream: expected a stream on {device}, got one on {stream.device}")
-        self.device, self.given = device, stream
-        self.stream = _stream_ptr(stream, device)
-        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+        try:
+            return torch._C._cuda_getCurrentRawStream(device.index)
+        except AttributeError:
+            return torch.cuda.current_stream(device).cuda_stream
+    if stream.device != device:
+        raise ValueError(f"stream: expected a stream on {device}, got one on {stream.device}")
+    return stream.cuda_stream
 
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self
 
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _call(device, fn, *args) -> None:
+    """fn(*args) with the device current; its status checked."""
+    import torch
+    if torch.cuda.current_device() == device.index:
+        status = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args)
+    if status != KLD_OK:
+        _check(status)
 
-    def empty(self, shape, dtype):
-        import torch
-        if self.given is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
-        with torch.cuda.stream(self.given):
-            return torch.empty(shape, dtype=dtype, device=self.device)
 
-    def workspace(self, given, nbytes):
-        import torch
-        if given is None:
-            return self.empty(max(nbytes, 1), torch.uint8)
-        if given.dtype != torch.uint8 or given.device != self.device or not given.is_contiguous() \
-                or given.numel() < nbytes:
-            raise ValueError(f"workspace: expected a contiguous uint8 tensor of >= {nbytes} bytes on {self.device}")
-        return given
+def _empty(shape, dtype, device, stream):
+    """Memory of the stream the call runs on: what other streams let go of may
+    still be in use there."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _workspace(given, nbytes, device, stream):
+    import torch
+    if given is None:
+        return _empty(max(nbytes, 1), torch.uint8, device, stream)
+    if given.dtype != torch.uint8 or given.device != device or not given.is_contiguous() or given.numel() < nbytes:
+        raise ValueError(f"workspace: expected a contiguous uint8 tensor of >= {nbytes} bytes on {device}")
+    return given
+
+
+@functools.lru_cache(maxsize=256)
+def _select_bytes(vocab, code, items, beams, k):
+    return kld_eval_beam_select_workspace(vocab, code, items, beams, k)
+
+
+@functools.lru_cache(maxsize=256)
+def _grad_bytes(vocab, dim, n):
+    return kld_eval_embed_grad_workspace(vocab, dim, n)
 
 
 def _rows_of(t, name, device, dtype=None):
@@ -708,6 +727,8 @@ def _rows_of(t, name, device, dtype=None):
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     n, m = t.shape
+    if t.is_contiguous():
+        return m
     if (m > 1 and t.stride(1) != 1) or (n > 1 and t.stride(0) < m):
         raise ValueError(f"{name}: expected rows of contiguous elements that do not overlap")
     return t.stride(0) if n > 1 else m
@@ -725,12 +746,12 @@ def _as_rows(t, n, dim, name):
 
 def _per(t, shape, dtype, name, device):
     """Address of a contiguous tensor of the given shape."""
+    if t.dtype == dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return t.data_ptr()
     if t.device != device:
         raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)}, got {t.dtype} "
-                         f"{tuple(t.shape)}")
-    return t.data_ptr()
+    raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)}, got {t.dtype} "
+                     f"{tuple(t.shape)}")
 
 
 def beam_workspace_bytes(vocab: int, n_items: int, n_beams: int, k: int, dtype="bf16") -> int:
@@ -754,36 +775,35 @@ def beam_select(logits, scores, k=None, finished=None, eos_token: int = -1, out=
     device = _device_of(logits, "logits")
     if scores.dim() != 2:
         raise ValueError("scores: expected an [items, beams] tensor")
-    items, beams = scores.shape
+    per_beam = scores.shape
+    items, beams = per_beam
     if logits.dim() == 3:
         if logits.shape[0] != items or logits.shape[1] != beams:
             raise ValueError(f"logits: expected [{items}, {beams}, vocab], got {tuple(logits.shape)}")
         if items > 1 and beams > 1 and logits.stride(0) != beams * logits.stride(1):
             raise ValueError("logits: the rows of all beams must be one stride apart")
-        rows = logits.as_strided((items * beams, logits.shape[2]),
-                                 (logits.stride(1) if beams > 1 else logits.stride(0), logits.stride(2)))
-    elif logits.dim() == 2 and logits.shape[0] == items * beams:
-        rows = logits
-    else:
+        logits = logits.as_strided((items * beams, logits.shape[2]),
+                                   (logits.stride(1) if beams > 1 else logits.stride(0), logits.stride(2)))
+    elif logits.dim() != 2 or logits.shape[0] != items * beams:
         raise ValueError(f"logits: expected [{items * beams}, vocab], got {tuple(logits.shape)}")
     code = _dtype_code(logits.dtype)
-    vocab = rows.shape[1]
+    vocab = logits.shape[1]
     k = beams if k is None else int(k)
-    stride = _rows_of(rows, "logits", device)
-    shape = torch.Size((items, max(k, 0)))
-    with _Launch(device, stream) as on:
-        nbytes = kld_eval_beam_select_workspace(vocab, code, items, beams, k)
-        f32, i32, u8 = torch.float32, torch.int32, torch.uint8
-        if out is None:
-            out = (on.empty(shape, f32), on.empty(shape, i32), on.empty(shape, i32), on.empty(shape, u8))
-        elif len(out) != 4:
-            raise ValueError("out: expected (scores, parents, tokens, finished)")
-        s, p, t, f = (_per(x, shape, dt, f"out[{i}]", device) for i, (x, dt) in enumerate(zip(out, (f32, i32, i32, u8))))
-        ws = on.workspace(workspace, nbytes)
-        kld_eval_beam_select(rows.data_ptr(), code, vocab, stride, items, beams, k,
-                             _per(scores, scores.shape, f32, "scores", device),
-                             0 if finished is None else _per(finished, scores.shape, u8, "finished", device),
-                             int(eos_token), s, p, t, f, ws.data_ptr(), ws.numel(), on.stream)
+    stride = _rows_of(logits, "logits", device)
+    nbytes = _select_bytes(vocab, code, items, beams, k)
+    shape = per_beam if k == beams else torch.Size((items, k))
+    f32, i32, u8 = torch.float32, torch.int32, torch.uint8
+    if out is None:
+        out = (_empty(shape, f32, device, stream), _empty(shape, i32, device, stream),
+               _empty(shape, i32, device, stream), _empty(shape, u8, device, stream))
+    s, p, t, f = out
+    ws = _workspace(workspace, nbytes, device, stream)
+    _call(device, load_library().kld_eval_beam_select, logits.data_ptr(), code, vocab, stride, items, beams, k,
+          _per(scores, per_beam, f32, "scores", device),
+          0 if finished is None else _per(finished, per_beam, u8, "finished", device), eos_token,
+          _per(s, shape, f32, "out[0]", device), _per(p, shape, i32, "out[1]", device),
+          _per(t, shape, i32, "out[2]", device), _per(f, shape, u8, "out[3]", device), ws.data_ptr(), ws.numel(),
+          _raw_stream(stream, device))
     return out
 
 
@@ -809,6 +829,17 @@ def _state_geometry(x, length_dim, name):
     return outer, step * e, size[length_dim], run * e, strides[0] * e
 
 
+def _geometry(x, length_dim, name):
+    if length_dim is None:
+        inner = x.numel() // x.shape[0] if x.numel() else 0
+        if inner and not x[0].is_contiguous():
+            raise ValueError(f"{name}: without length_dim each beam's state must be contiguous")
+        return 1, 0, 1, inner * x.element_size(), x.stride(0) * x.element_size()
+    if not 0 < length_dim < x.dim():
+        raise ValueError(f"{name}: length_dim must be one of its dimensions behind the first")
+    return _state_geometry(x, length_dim, name) if x.numel() else (0, 0, 0, 0, 0)
+
+
 def beam_reorder(states, parents, lengths=None, length_dim=None, stream=None) -> None:
     """The beams' states follow the chosen beams, in place: state row
     i * beams + w becomes what row i * beams + parents[i, w] was (a parent of
@@ -828,28 +859,22 @@ def beam_reorder(states, parents, lengths=None, length_dim=None, stream=None) ->
     items, beams = parents.shape
     if (lengths is None) != (length_dim is None):
         raise ValueError("lengths and length_dim: give both or neither")
-    groups = {}
+    n, groups = items * beams, {}
     for i, x in enumerate(states):
-        name = f"states[{i}]"
-        if x.device != device:
-            raise ValueError(f"{name}: expected a tensor on {device}, got {x.device}")
-        if x.dim() < 1 or x.shape[0] != items * beams:
-            raise ValueError(f"{name}: expected [{items * beams}, ...], got {tuple(x.shape)}")
-        if length_dim is None:
-            inner = x.numel() // x.shape[0] if x.numel() else 0
-            if inner and not x[0].is_contiguous():
-                raise ValueError(f"{name}: without length_dim each beam's state must be contiguous")
-            geometry = (1, 0, 1, inner * x.element_size(), x.stride(0) * x.element_size())
+        shape = x.shape
+        if x.device != device or not shape or shape[0] != n:
+            raise ValueError(f"states[{i}]: expected [{n}, ...] on {device}, got {tuple(shape)} on {x.device}")
+        key = (shape, x.stride(), x.element_size())
+        if key in groups:
+            groups[key][1].append(x.data_ptr())
         else:
-            if not 0 < length_dim < x.dim():
-                raise ValueError(f"{name}: length_dim must be one of its dimensions behind the first")
-            geometry = _state_geometry(x, length_dim, name) if x.numel() else (0, 0, 0, 0, 0)
-        groups.setdefault(geometry, []).append(x.data_ptr())
-    with _Launch(device, stream) as on:
-        pa = _per(parents, parents.shape, torch.int32, "parents", device)
-        le = 0 if lengths is None else _per(lengths, torch.Size((items,)), torch.int32, "lengths", device)
-        for (outer, step, positions, nbytes, beam), ptrs in groups.items():
-            kld_eval_beam_reorder(ptrs, items, beams, pa, beam, outer, step, positions, nbytes, le, on.stream)
+            groups[key] = (_geometry(x, length_dim, f"states[{i}]"), [x.data_ptr()])
+    pa = _per(parents, parents.shape, torch.int32, "parents", device)
+    le = 0 if lengths is None else _per(lengths, torch.Size((items,)), torch.int32, "lengths", device)
+    raw = _raw_stream(stream, device)
+    for (outer, step, positions, nbytes, beam), ptrs in groups.values():
+        _call(device, load_library().kld_eval_beam_reorder, (ctypes.c_void_p * len(ptrs))(*ptrs), len(ptrs), items,
+              beams, pa, beam, outer, step, positions, nbytes, le, raw)
 
 
 def _token_ids(tokens, device):
@@ -878,18 +903,19 @@ def embed(table, tokens, scale: float = 1.0, out=None, dtype=None, stream=None):
     stride = _rows_of(table, "table", device)
     vocab, dim = table.shape
     n, tk = tokens.numel(), _token_ids(tokens, device)
-    with _Launch(device, stream) as on:
-        if out is None:
-            out = on.empty((*tokens.shape, dim), _torch_dtype(code if dtype is None else _dtype_code(dtype)))
-        else:
-            if dtype is not None and out.dtype != _torch_dtype(_dtype_code(dtype)):
-                raise TypeError(f"out: expected {_torch_dtype(_dtype_code(dtype))}, got {out.dtype}")
-            if tuple(out.shape) != (*tokens.shape, dim):
-                raise ValueError(f"out: expected shape {(*tokens.shape, dim)}, got {tuple(out.shape)}")
-        rows = _as_rows(out, n, dim, "out")
-        ostride = _rows_of(rows, "out", device)
-        kld_eval_embed(table.data_ptr(), code, vocab, dim, stride, tk, n, scale, rows.data_ptr(),
-                       _dtype_code(out.dtype), ostride, on.stream)
+    if out is None:
+        ocode = code if dtype is None else _dtype_code(dtype)
+        out = _empty((*tokens.shape, dim), _torch_dtype(ocode), device, stream)
+        o, ostride = out.data_ptr(), dim
+    else:
+        ocode = _dtype_code(out.dtype)
+        if dtype is not None and ocode != _dtype_code(dtype):
+            raise TypeError(f"out: expected {_torch_dtype(_dtype_code(dtype))}, got {out.dtype}")
+        if tuple(out.shape) != (*tokens.shape, dim):
+            raise ValueError(f"out: expected shape {(*tokens.shape, dim)}, got {tuple(out.shape)}")
+        o, ostride = out.data_ptr(), _rows_of(_as_rows(out, n, dim, "out"), "out", device)
+    _call(device, load_library().kld_eval_embed, table.data_ptr(), code, vocab, dim, stride, tk, n, scale, o, ocode,
+          ostride, _raw_stream(stream, device))
     return out
 
 
@@ -915,15 +941,16 @@ def embed_grad(grad, tokens, vocab: int, scale: float = 1.0, out=None, dtype="f3
     rows = _as_rows(grad, n, dim, "grad")
     gcode, gstride = _dtype_code(grad.dtype), _rows_of(rows, "grad", device)
     tk = _token_ids(tokens, device)
-    with _Launch(device, stream) as on:
-        if out is None:
-            out = on.empty((vocab, dim), _torch_dtype(_dtype_code(dtype)))
-        elif tuple(out.shape) != (vocab, dim):
-            raise ValueError(f"out: expected shape {(vocab, dim)}, got {tuple(out.shape)}")
-        ostride = _rows_of(out, "out", device)
-        ws = on.workspace(workspace, kld_eval_embed_grad_workspace(vocab, dim, n))
-        kld_eval_embed_grad(rows.data_ptr(), gcode, gstride, tk, n, vocab, dim, scale, out.data_ptr(),
-                            _dtype_code(out.dtype), ostride, accumulate, ws.data_ptr(), ws.numel(), on.stream)
+    nbytes = _grad_bytes(vocab, dim, n)
+    if out is None:
+        out = _empty((vocab, dim), _torch_dtype(_dtype_code(dtype)), device, stream)
+    elif tuple(out.shape) != (vocab, dim):
+        raise ValueError(f"out: expected shape {(vocab, dim)}, got {tuple(out.shape)}")
+    ostride = _rows_of(out, "out", device)
+    ws = _workspace(workspace, nbytes, device, stream)
+    _call(device, load_library().kld_eval_embed_grad, rows.data_ptr(), gcode, gstride, tk, n, vocab, dim, scale,
+          out.data_ptr(), _dtype_code(out.dtype), ostride, 1 if accumulate else 0, ws.data_ptr(), ws.numel(),
+          _raw_stream(stream, device))
     return out
 
 
