@@ -4,17 +4,18 @@
 // With s_w the score of beam w and z its logit row, a live beam offers token v
 // at s_w + z_v - lse_w, lse_w = log sum exp z over the row's finite entries; a
 // finished beam offers itself alone, at s_w. Of one beam's candidates the order
-// is that of its logits (equal logits: the lowest id first), so a row's K
-// largest logits hold all that can be chosen from it, and a slice's K largest
-// all that can be chosen from the slice.
+// is that of its logits (equal logits: the lowest id first).
 //
-// Two launches. The scan reads every live row once: each wave streams one slice
-// of a row, keeps the sum of exponentials against a running maximum and the
-// slice's K largest logits. The merge joins the slices of an item's beams,
-// forms the normalisers and scores in float64 and ranks the candidates. Its
-// normalisers come from float32 exponentials; where two neighbours of the
-// ranking, of different beams, are closer than those can tell, the item's
-// workgroup reads its rows again in float64 and ranks once more.
+// Two launches. The scan streams every live row once and keeps nothing but the
+// sum of its exponentials and the largest logit of each group of consecutive
+// elements (128 of bfloat16, 64 of float32). The merge forms the item's
+// normalisers, finds the K best groups -- ordered by their largest logit, equal
+// ones by beam and place, they hold every chosen candidate -- reads those groups
+// again and ranks their elements in float64. The normalisers come from float32
+// exponentials; where two neighbours of the ranking, of different beams, are
+// closer than those can tell, the item's workgroup reads the rows concerned
+// again in float64 and ranks once more.
+#include <float.h>
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -24,39 +25,38 @@
 namespace kldk {
 namespace {
 
-constexpr int kWaves = 4;        // waves per scan workgroup; they share nothing
-constexpr int kChunks = 4;       // 16-byte chunks per lane and tile
+constexpr int kWaves = 4;            // waves per scan workgroup; they share nothing
+constexpr int kChunks = 4;           // 16-byte chunks per lane and tile
 constexpr int kTile = 64 * kChunks;  // chunks of a tile
-constexpr int kList = 256;       // candidates a wave holds before it must drop some
-constexpr int kMergeThreads = 256;
-constexpr int kHold = 8;         // candidates a merge thread keeps in registers
-constexpr int kMergeList = 1024;  // candidates the merge ranks at once
+constexpr int kGroupChunks = 16;     // chunks of a group: those of 16 neighbouring lanes
+constexpr int kTileGroups = kTile / kGroupChunks;
+constexpr int64_t kTargetWaves = 8192;
+constexpr int kMergeThreads = 512;
+constexpr int kMergeList = 1024;     // candidates the merge ranks at once
+constexpr int kHold = 6;             // quadruples of groups that a merge thread keeps in registers
+constexpr int kNear = 512;           // groups that the merge reads again at most
 
 constexpr float kLog2e = 1.44269504088896340736f;
 // Bounds of the float32 reference. Logits above the first, or rows that lie
 // below the second altogether, would lose their sums in float32: the merge
 // takes such rows in float64.
-constexpr float kMostLogit = 1048576.0f;
+constexpr float kMostRef = 1048576.0f * kLog2e;
 constexpr float kLeastRef = -32768.0f * kLog2e;
 
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
-
-struct Cand {
-    float z;
-    int v;  // -1: none
-};
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 // Sum of a slice: sum 2^(z log2e - ref) over its finite logits. A NaN sum:
-// the slice holds logits past kMostLogit.
+// the slice holds logits past kMostRef.
 struct Slice {
     double sum;
     float ref;
-    int n;  // candidates found in it
+    int unused;
 };
 
 struct Layout {
     Slice* slice;  // [rows][slices]
-    Cand* cand;    // [rows][slices][k]
+    float* top;    // [rows][groups], in the order of their elements
 };
 
 template <class E>
@@ -69,228 +69,133 @@ struct Elem<uint16_t> {
         const unsigned int w = c[e >> 1];
         return __uint_as_float(e & 1 ? w & 0xffff0000u : w << 16);
     }
-    static __device__ __forceinline__ void set(u32x4& c, int e, uint16_t x) {
-        const unsigned int w = c[e >> 1];
-        c[e >> 1] = e & 1 ? (w & 0xffffu) | (static_cast<unsigned int>(x) << 16) : (w & 0xffff0000u) | x;
-    }
-    static __device__ __forceinline__ uint16_t none() { return 0xff80u; }
 };
 template <>
 struct Elem<float> {
     static constexpr int kPer = 4;
     static constexpr unsigned int kNone = 0xff800000u;
     static __device__ __forceinline__ float get(const u32x4& c, int e) { return __uint_as_float(c[e]); }
-    static __device__ __forceinline__ void set(u32x4& c, int e, float x) { c[e] = __float_as_uint(x); }
-    static __device__ __forceinline__ float none() { return -INFINITY; }
 };
 
 __device__ __forceinline__ float widen(float x) { return x; }
 __device__ __forceinline__ float widen(uint16_t b) { return __uint_as_float(static_cast<unsigned int>(b) << 16); }
 
-// Unsigned order of float values, -0 and 0 alike (none is NaN).
-__device__ __forceinline__ unsigned int order_of(float z) {
-    const unsigned int u = __float_as_uint(z + 0.0f);
-    return u & 0x80000000u ? ~u : u | 0x80000000u;
-}
-__device__ __forceinline__ float value_of(unsigned int o) {
-    return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
-}
-// Of two candidates of one row the one with the larger key comes first.
-__device__ __forceinline__ uint64_t key_of(float z, int v) {
-    return (static_cast<uint64_t>(order_of(z)) << 32) | (0xffffffffu - static_cast<unsigned int>(v));
-}
+// A row: `head` elements before the first 16-byte boundary, whole chunks, and
+// the elements behind the last of them; the ones outside the chunks are loose.
+template <class E>
+struct Row {
+    const E* p;
+    int head;
+    int chunks;
+    int tail_at;
+    int loose;
+    __device__ __forceinline__ Row(const E* row, int64_t vocab) : p(row) {
+        constexpr int kPer = Elem<E>::kPer;
+        const int to_chunk = static_cast<int>(-(reinterpret_cast<uintptr_t>(row) / sizeof(E)) & (kPer - 1));
+        head = to_chunk < vocab ? to_chunk : static_cast<int>(vocab);
+        chunks = static_cast<int>((vocab - head) / kPer);
+        tail_at = head + chunks * kPer;
+        loose = head + static_cast<int>(vocab - tail_at);
+    }
+    __device__ __forceinline__ int loose_id(int i) const { return i < head ? i : tail_at + (i - head); }
+};
 
-// The k best of the wave's n candidates (n <= kList), in order, at the list's
-// front; each lane ranks up to kList / 64 of them against all.
-__device__ __forceinline__ int keep_best(uint64_t* list, int n, int k, int lane) {
-    constexpr int kMine = kList / 64;
-    uint64_t mine[kMine];
-    int rank[kMine];
-#pragma unroll
-    for (int q = 0; q < kMine; ++q) {
-        mine[q] = q * 64 + lane < n ? list[q * 64 + lane] : 0;
-        rank[q] = 0;
-    }
-    for (int i = 0; i < n; ++i) {
-        const uint64_t other = list[i];
-#pragma unroll
-        for (int q = 0; q < kMine; ++q)
-            if (q * 64 < n) rank[q] += other > mine[q];
-    }
-    __builtin_amdgcn_wave_barrier();
-#pragma unroll
-    for (int q = 0; q < kMine; ++q)
-        if (q * 64 + lane < n && rank[q] < k) list[rank[q]] = mine[q];
-    __builtin_amdgcn_wave_barrier();
-    return n < k ? n : k;
+// Maximum over the 16 lanes of a row: with the neighbour, the other pair of the
+// quad, the other quad of the half, the other half.
+template <int kCtrl>
+__device__ __forceinline__ float max_with(float x) {
+    return fmaxf(x, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), kCtrl, 0xf, 0xf, true)));
 }
-
-// A value that at least k lanes reach (none: -inf), from the upper 16 bits of
-// the k-th largest lane value: the k-th largest of a superset is no smaller.
-__device__ __forceinline__ float reached_by(float x, int k) {
-    const unsigned int o = order_of(x);
-    unsigned int t = 0;
-#pragma unroll
-    for (int b = 31; b >= 16; --b) {
-        const unsigned int c = t | (1u << b);
-        if (__popcll(__ballot(o >= c)) >= k) t = c;
-    }
-    const float v = value_of(t);
-    return v > -INFINITY ? v : -INFINITY;   // also where the bits say NaN: fewer than k lanes hold a finite value
+__device__ __forceinline__ float row_max(float x) {
+    return max_with<0x140>(max_with<0x141>(max_with<0x4e>(max_with<0xb1>(x))));
 }
 
 template <class E>
 __global__ void __launch_bounds__(kWaves * 64)
     beam_scan_kernel(const E* __restrict__ logits, int64_t vocab, int64_t row_stride, int64_t rows, int slices,
-                     int tiles_per_slice, int k, int drop_at, const float* __restrict__ scores,
+                     int tiles, int tiles_per_slice, const float* __restrict__ scores,
                      const uint8_t* __restrict__ finished, Layout out) {
     constexpr int kPer = Elem<E>::kPer;
     constexpr int kEach = kChunks * kPer;  // elements per lane and tile
-    __shared__ uint64_t lists[kWaves][kList];
-    __shared__ u32x4 stages[kWaves][64 * kChunks];
-    __shared__ int owners[kWaves][64];
     const int lane = threadIdx.x & 63;
-    const int64_t task = static_cast<int64_t>(blockIdx.x) * kWaves + (threadIdx.x >> 6);
+    const int64_t task = static_cast<int64_t>(blockIdx.x) * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t row = task / slices;
     if (row >= rows) return;
     const int slice = static_cast<int>(task - row * slices);
-    const float score = scores[row];
-    if (!isfinite(score) || (finished && finished[row])) return;  // its logits offer nothing
-    uint64_t* list = lists[threadIdx.x >> 6];
-    u32x4* stage = stages[threadIdx.x >> 6];
-    int* owner = owners[threadIdx.x >> 6];
+    const Row<E> in(logits + row * row_stride, vocab);
+    const u32x4* body = reinterpret_cast<const u32x4*>(in.p + in.head) + lane;
+    const int t0 = slice * tiles_per_slice;
+    const int t1 = t0 + tiles_per_slice < tiles ? t0 + tiles_per_slice : tiles;
 
-    // chunk c of the row: elements [c kPer - off, c kPer - off + kPer), 16-byte aligned
-    const E* p = logits + row * row_stride;
-    const int off = static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(E));
-    const E* base = p - off;
-    const int64_t chunks = (vocab + off + kPer - 1) / kPer;
-    const int64_t full_from = off ? 1 : 0, full_to = (vocab + off) / kPer;  // chunks that lie in the row as a whole
-    const int64_t c_first = static_cast<int64_t>(slice) * tiles_per_slice * kTile;
-    int64_t c_last = c_first + static_cast<int64_t>(tiles_per_slice) * kTile;
-    if (c_last > chunks) c_last = chunks;
-
-    const auto load = [&](int64_t c0, u32x4(&r)[kChunks]) {
-        if (c0 >= full_from && c0 + kTile <= full_to && c0 + kTile <= c_last) {
+    u32x4 r[kChunks];
+    const auto load = [&](int tile) {
+        const int c0 = tile * kTile;
+        if (c0 + kTile <= in.chunks) {
 #pragma unroll
-            for (int u = 0; u < kChunks; ++u)
-                r[u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(base + (c0 + u * 64 + lane) * kPer));
+            for (int u = 0; u < kChunks; ++u) r[u] = __builtin_nontemporal_load(body + c0 + u * 64);
         } else {
+            const int left = in.chunks - c0 - lane;
 #pragma unroll
             for (int u = 0; u < kChunks; ++u) {
-                const int64_t c = c0 + u * 64 + lane;
                 const unsigned int none = Elem<E>::kNone;
                 r[u] = u32x4{none, none, none, none};
-                if (c < c_last) {
-                    if (c >= full_from && c < full_to) {
-                        r[u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(base + c * kPer));
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < kPer; ++e) {
-                            const int64_t i = c * kPer + e - off;
-                            if (i >= 0 && i < vocab) Elem<E>::set(r[u], e, p[i]);
-                        }
-                    }
-                }
+                if (u * 64 < left) r[u] = __builtin_nontemporal_load(body + c0 + u * 64);
             }
         }
     };
+    if (t0 < t1) load(t0);
+    // a row that offers nothing: known after its first tile is on its way
+    if (!isfinite(scores[row]) || (finished && finished[row])) return;
 
-    float ref = kLeastRef;  // in binary units
+    // the first four lanes of each row of 16 store its maxima, a chunk each
+    float* top = out.top + (row * tiles + t0) * kTileGroups + (lane & 3) * (kTileGroups / kChunks) + (lane >> 4);
+    float ref = kLeastRef;  // of this lane, in binary units
     double sum = 0.0;
-    bool wild = false;
-    float least = -INFINITY;  // a logit below it is no candidate
-    uint64_t least_key = 0;
-    int n = 0;
-    u32x4 r[kChunks], next[kChunks];
-    if (c_first < c_last) load(c_first, r);
-    for (int64_t c0 = c_first; c0 < c_last; c0 += kTile) {
-        const bool more = c0 + kTile < c_last;
-        if (more) load(c0 + kTile, next);
-
-        float best, part, to;
+    for (int tile = t0; tile < t1; ++tile) {
+        float x[kEach];
+#pragma unroll
+        for (int u = 0; u < kChunks; ++u)
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) x[u * kPer + e] = Elem<E>::get(r[u], e);
+        if (tile + 1 < t1) load(tile + 1);
+        float best[kChunks], part, to;
         for (bool clean = false;; clean = true) {
-            best = -INFINITY;
 #pragma unroll
             for (int u = 0; u < kChunks; ++u) {
+                best[u] = x[u * kPer];
 #pragma unroll
-                for (int e = 0; e < kPer; ++e) best = fmaxf(best, Elem<E>::get(r[u], e));
+                for (int e = 1; e < kPer; ++e) best[u] = fmaxf(best[u], x[u * kPer + e]);
             }
-            to = fmaxf(ref, best * kLog2e);
+            to = fmaxf(ref, fmaxf(fmaxf(best[0], best[1]), fmaxf(best[2], best[3])) * kLog2e);
             float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int u = 0; u < kChunks; ++u)
-#pragma unroll
-                for (int e = 0; e < kPer; ++e)
-                    acc[e & 3] += __builtin_amdgcn_exp2f(__builtin_fmaf(Elem<E>::get(r[u], e), kLog2e, -to));
+            for (int i = 0; i < kEach; ++i) acc[i & 3] += __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], kLog2e, -to));
             part = (acc[0] + acc[1]) + (acc[2] + acc[3]);
-            // a NaN among the logits makes the sum NaN, an infinity or a logit too large shows in the largest
-            if (clean || !__ballot(!(part >= 0.0f) || !(best <= kMostLogit))) break;
+            // a NaN or an infinity among the logits makes the sum NaN: exclude them
+            if (clean || !__ballot(!(part >= 0.0f))) break;
 #pragma unroll
-            for (int u = 0; u < kChunks; ++u)
-#pragma unroll
-                for (int e = 0; e < kPer; ++e)
-                    if (!isfinite(Elem<E>::get(r[u], e))) Elem<E>::set(r[u], e, Elem<E>::none());
+            for (int i = 0; i < kEach; ++i) x[i] = isfinite(x[i]) ? x[i] : -INFINITY;
         }
-        wild |= !(best <= kMostLogit);
         sum = sum * static_cast<double>(__builtin_amdgcn_exp2f(ref - to)) + static_cast<double>(part);
         ref = to;
-
-        if (c0 == c_first) {
-            least = reached_by(best, k);
-            least_key = least > -INFINITY ? static_cast<uint64_t>(order_of(least)) << 32 : 0;
-        }
-        // Lanes that hold a candidate lay their elements side by side, then the
-        // whole wave looks at them, one element per lane.
-        const bool hit = best >= least && best > -INFINITY;
-        const unsigned long long hits = __ballot(hit);
-        if (hits) {
-            if (hit) {
-                const int slot = __popcll(hits & ((1ull << lane) - 1));
-                owner[slot] = lane;
+        float mine = row_max(best[0]);
 #pragma unroll
-                for (int u = 0; u < kChunks; ++u) stage[slot * kChunks + u] = r[u];
-            }
-            __builtin_amdgcn_wave_barrier();
-            const int held = __popcll(hits) * kEach;
-            for (int i0 = 0; i0 < held; i0 += 64) {
-                const int i = i0 + lane;
-                const int e = i % kEach;
-                const bool there = i < held;
-                const float z = there ? widen(reinterpret_cast<const E*>(stage)[i]) : -INFINITY;
-                const int64_t chunk = c0 + (e / kPer) * 64 + (there ? owner[i / kEach] : 0);
-                const uint64_t key = key_of(z, static_cast<int>(chunk * kPer + e % kPer - off));
-                const bool in = z > -INFINITY && key > least_key;
-                const unsigned long long b = __ballot(in);
-                if (!b) continue;
-                if (in) list[n + __popcll(b & ((1ull << lane) - 1))] = key;
-                n += __popcll(b);
-                __builtin_amdgcn_wave_barrier();
-                if (n > kList - 64) {
-                    n = keep_best(list, n, k, lane);
-                    least_key = list[k - 1];
-                    least = value_of(static_cast<unsigned int>(least_key >> 32));
-                }
-            }
-            if (n >= drop_at) {
-                n = keep_best(list, n, k, lane);
-                if (n == k) {
-                    least_key = list[k - 1];
-                    least = value_of(static_cast<unsigned int>(least_key >> 32));
-                }
-            }
+        for (int u = 1; u < kChunks; ++u) {
+            const float q = row_max(best[u]);
+            mine = (lane & 3) == u ? q : mine;
         }
-#pragma unroll
-        for (int u = 0; u < kChunks; ++u) r[u] = next[u];
+        static_assert(kChunks == 4 && kGroupChunks == 16, "");
+        if ((lane & 12) == 0) *top = mine;
+        top += kTileGroups;
     }
-
-    n = keep_best(list, n, k, lane);
-    if (lane < k) {
-        const uint64_t key = lane < n ? list[lane] : 0;
-        out.cand[(row * slices + slice) * k + lane] =
-            lane < n ? Cand{value_of(static_cast<unsigned int>(key >> 32)),
-                            static_cast<int>(0xffffffffu - static_cast<unsigned int>(key))}
-                     : Cand{-INFINITY, -1};
+    if (slice == 0 && lane < in.loose) {
+        const float z = widen(in.p[in.loose_id(lane)]);
+        if (isfinite(z)) {
+            const float to = fmaxf(ref, z * kLog2e);
+            sum = sum * static_cast<double>(__builtin_amdgcn_exp2f(ref - to)) +
+                  static_cast<double>(__builtin_amdgcn_exp2f(__builtin_fmaf(z, kLog2e, -to)));
+            ref = to;
+        }
     }
     float whole = ref;
 #pragma unroll
@@ -298,11 +203,11 @@ __global__ void __launch_bounds__(kWaves * 64)
     sum *= static_cast<double>(__builtin_amdgcn_exp2f(ref - whole));
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o);
-    wild = __ballot(wild) != 0;
-    if (lane == 0) out.slice[row * slices + slice] = Slice{wild ? static_cast<double>(NAN) : sum, whole, n};
+    if (lane == 0) out.slice[row * slices + slice] = Slice{whole <= kMostRef ? sum : static_cast<double>(NAN), whole, 0};
 }
 
-// A scored candidate and the order of the selection.
+// A scored candidate and the order of the selection. For a group, z is its
+// largest logit and v its place among the row's groups.
 struct Scored {
     double s;
     float z;
@@ -316,236 +221,409 @@ __device__ __forceinline__ bool before(const Scored& a, const Scored& b) {
     return a.v < b.v;
 }
 
-__device__ __forceinline__ unsigned int order_hi(double s) {
-    const uint64_t u = static_cast<uint64_t>(__double_as_longlong(s));
-    return static_cast<unsigned int>((u >> 63 ? ~u : u | (uint64_t{1} << 63)) >> 32);
+__device__ __forceinline__ unsigned int order_of(float z) {
+    const unsigned int u = __float_as_uint(z);
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
-__device__ __forceinline__ double value_hi(unsigned int o) {
-    const uint64_t u = static_cast<uint64_t>(o) << 32;
-    return __longlong_as_double(static_cast<long long>(u >> 63 ? u ^ (uint64_t{1} << 63) : ~u));
+__device__ __forceinline__ float value_of(unsigned int o) {
+    return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
+}
+// Values that `few` and that `many` of the wave's lanes reach, from the upper 16
+// bits of the few-th and many-th largest; -inf where fewer lanes hold a finite one.
+__device__ __forceinline__ float2 reached_by(float x, int few, int many) {
+    const unsigned int o = order_of(x);
+    unsigned int a = 0, b = 0;
+#pragma unroll 2
+    for (unsigned int bit = 1u << 31; bit >= 1u << 16; bit >>= 1) {
+        a |= __popcll(__ballot(o >= (a | bit))) >= few ? bit : 0;
+        b |= __popcll(__ballot(o >= (b | bit))) >= many ? bit : 0;
+    }
+    const float va = value_of(a), vb = value_of(b);  // NaN below the lowest finite value
+    return float2{va > -INFINITY ? va : -INFINITY, vb > -INFINITY ? vb : -INFINITY};
+}
+
+enum : int { kEmpty, kLive, kFinished, kRetake, kExact };  // kRetake: live, its normaliser is to be taken in float64
+
+struct Merge {
+    float score[kBeamMaxBeams];
+    double lse[kBeamMaxBeams];
+    float shift[kBeamMaxBeams];  // score - lse, rounded; -inf for a beam that offers no logits
+    int state[kBeamMaxBeams];
+    f32x4 quad[kNear];           // quadruples with groups worth reading,
+    int2 quad_at[kNear];         // their beams and first groups
+    int2 near[kNear];            // those groups: beam, place
+    double list_s[kMergeList];   // candidates: score,
+    float list_z[kMergeList];    // logit,
+    int2 list_wv[kMergeList];    // beam and id
+    Scored ranked[kBeamMaxSelect + 1];
+    Scored pick[kMergeThreads / 64];
+    double part[kMergeThreads / 64];
+    float bound[kMergeThreads / 64][2];
+    int count, quad_count, near_count, again;
+    __device__ __forceinline__ void set_shift(int w) {
+        shift[w] = live(w) ? static_cast<float>(score[w] - lse[w]) : -INFINITY;
+    }
+    __device__ __forceinline__ bool live(int w) const { return state[w] == kLive || state[w] == kExact; }
+    __device__ __forceinline__ Scored scored(float z, int w, int v) const {
+        return Scored{score[w] + (static_cast<double>(z) - lse[w]), z, w, v};
+    }
+    __device__ __forceinline__ void add(const Scored& c) {
+        const int at = atomicAdd(&count, 1);
+        if (at >= kMergeList) return;
+        list_s[at] = c.s;
+        list_z[at] = c.z;
+        list_wv[at] = int2{c.w, c.v};
+    }
+    __device__ __forceinline__ Scored listed(int i) const {
+        return Scored{list_s[i], list_z[i], list_wv[i].x, list_wv[i].y};
+    }
+    // The list's first m entries in order; four lanes per entry.
+    __device__ __forceinline__ void rank(int n, int m) {
+        const int t = threadIdx.x;
+#pragma unroll 1
+        for (int i0 = 0; i0 < n; i0 += kMergeThreads / 4) {
+            const int i = i0 + (t >> 2);
+            int at = 0;
+            Scored c{};
+            if (i < n) {
+                c = listed(i);
+#pragma unroll 4
+                for (int j = t & 3; j < n; j += 4) {
+                    const double other = list_s[j];
+                    at += other > c.s || (other == c.s && before(listed(j), c));
+                }
+            }
+            at += __shfl_xor(at, 1);
+            at += __shfl_xor(at, 2);
+            if (i < n && (t & 3) == 0 && at < m) ranked[at] = c;
+        }
+    }
+};
+
+// The item as its workgroup sees it.
+template <class E>
+struct Item {
+    const E* rows;
+    int64_t row_stride;
+    int64_t vocab;
+    int n_beams;
+    int groups;
+    int eos;
+    const float* tops;
+    __device__ __forceinline__ Row<E> row(int w) const { return Row<E>(rows + w * row_stride, vocab); }
+    // Candidates that no group holds: finished beams and loose elements.
+    template <class F>
+    __device__ __forceinline__ void each_loose(const Merge& s, F&& f) const {
+#pragma unroll 1
+        for (int i = threadIdx.x; i < n_beams * 16; i += kMergeThreads) {
+            const int w = i >> 4, q = i & 15;
+            if (s.state[w] == kFinished) {
+                if (q == 0) f(Scored{static_cast<double>(s.score[w]), 0.0f, w, eos});
+            } else if (s.live(w)) {
+                const Row<E> r = row(w);
+                if (q >= r.loose) continue;
+                const int v = r.loose_id(q);
+                const float z = widen(r.p[v]);
+                if (isfinite(z)) f(s.scored(z, w, v));
+            }
+        }
+    }
+};
+
+// The rare parts of the merge stand in functions of their own, so that what
+// every call runs stays small: a merge is as long as its instructions take to
+// arrive.
+
+// Normalisers in float64, of every beam whose state asks for it.
+template <class E>
+__device__ __attribute__((noinline)) void retake(Merge& s, const Item<E>& item) {
+    constexpr int kW = kMergeThreads / 64;
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    for (int w = 0; w < item.n_beams; ++w) {
+        if (s.state[w] != kRetake) continue;
+        const Row<E> row = item.row(w);
+        float most = -INFINITY;
+        double sum = 0.0;
+        for (int i = t; i < item.groups; i += kMergeThreads)
+            most = fmaxf(most, item.tops[static_cast<int64_t>(w) * item.groups + i]);
+        if (t < row.loose) {
+            const float z = widen(row.p[row.loose_id(t)]);
+            if (isfinite(z)) most = fmaxf(most, z);
+        }
+        for (int o = 32; o >= 1; o >>= 1) most = fmaxf(most, __shfl_xor(most, o));
+        __syncthreads();
+        if (lane == 0) s.part[wave] = most;
+        __syncthreads();
+        for (int q = 0; q < kW; ++q) most = fmaxf(most, static_cast<float>(s.part[q]));
+        for (int64_t i = most > -INFINITY ? t : item.vocab; i < item.vocab; i += kMergeThreads) {
+            const float z = widen(row.p[i]);
+            if (isfinite(z)) sum += exp(static_cast<double>(z) - most);
+        }
+        for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o);
+        __syncthreads();
+        if (lane == 0) s.part[wave] = sum;
+        __syncthreads();
+        if (t == 0) {
+            sum = 0.0;
+            for (int q = 0; q < kW; ++q) sum += s.part[q];
+            s.lse[w] = most + log(sum);
+            s.state[w] = most > -INFINITY ? kExact : kEmpty;  // empty: every logit is excluded
+            s.set_shift(w);
+        }
+    }
+    __syncthreads();
+}
+
+// Too many candidates near one another (long ties): the first m <= most one
+// after the other. A group is looked into where its largest logit beats what
+// the thread has found. Returns m.
+template <class E>
+__device__ __attribute__((noinline)) int pick_slowly(Merge& s, const Item<E>& item, int most) {
+    constexpr int kW = kMergeThreads / 64, kPer = Elem<E>::kPer, kOfGroup = kGroupChunks * kPer;
+    const Scored none{-INFINITY, -INFINITY, 0x7fffffff, 0x7fffffff};
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    for (int j = 0; j < most; ++j) {
+        Scored best = none;
+        const auto consider = [&](const Scored& c) {
+            if ((j == 0 || before(s.ranked[j - 1], c)) && before(c, best)) best = c;
+        };
+        for (int w = 0; w < item.n_beams; ++w) {
+            if (!s.live(w)) continue;
+            const Row<E> row = item.row(w);
+            for (int i = t; i < item.groups; i += kMergeThreads) {
+                const float z = item.tops[static_cast<int64_t>(w) * item.groups + i];
+                if (!(z > -INFINITY) || !(s.scored(z, w, 0).s > best.s || (best.w == w && z > best.z))) continue;
+                for (int e = 0; e < kOfGroup; ++e) {
+                    const int64_t v = row.head + int64_t{i} * kOfGroup + e;
+                    if (v >= row.tail_at) break;
+                    const float x = widen(row.p[v]);
+                    if (isfinite(x)) consider(s.scored(x, w, static_cast<int>(v)));
+                }
+            }
+        }
+        item.each_loose(s, consider);
+        for (int d = 32; d >= 1; d >>= 1) {
+            const Scored other{__shfl_xor(best.s, d), __shfl_xor(best.z, d), __shfl_xor(best.w, d),
+                               __shfl_xor(best.v, d)};
+            if (before(other, best)) best = other;
+        }
+        __syncthreads();
+        if (lane == 0) s.pick[wave] = best;
+        __syncthreads();
+        for (int q = 0; q < kW; ++q)
+            if (before(s.pick[q], best)) best = s.pick[q];
+        if (best.w == none.w) return j;
+        if (t == 0) s.ranked[j] = best;
+        __syncthreads();
+    }
+    return most;
 }
 
 template <class E>
 __global__ void __launch_bounds__(kMergeThreads)
     beam_merge_kernel(const E* __restrict__ logits, int64_t vocab, int64_t row_stride, int n_beams, int slices,
-                      int group, int k, double tol, const float* scores, const uint8_t* finished, int eos, Layout in,
-                      float* scores_out, int32_t* __restrict__ parents_out, int32_t* __restrict__ tokens_out,
-                      uint8_t* finished_out) {
+                      int group, int tiles, int loose, int k, double tol, const float* scores, const uint8_t* finished, int eos,
+                      Layout in, float* scores_out, int32_t* __restrict__ parents_out,
+                      int32_t* __restrict__ tokens_out, uint8_t* finished_out) {
     constexpr int kW = kMergeThreads / 64;
-    enum { kEmpty, kLive, kFinished, kRetake, kExact };  // kRetake: live, its normaliser is to be taken in float64
-    __shared__ float score[kBeamMaxBeams];
-    __shared__ double lse[kBeamMaxBeams];
-    __shared__ int state[kBeamMaxBeams];
-    __shared__ Scored list[kMergeList];
-    __shared__ Scored ranked[kBeamMaxSelect + 1];
-    __shared__ double dred[kW];
-    __shared__ unsigned int bound[kW];
-    __shared__ Scored pick[kW];
-    __shared__ int count, again;
-    const int64_t item = blockIdx.x;
+    constexpr int kPer = Elem<E>::kPer;
+    __shared__ Merge s;
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-    const int per = slices * k, total = n_beams * per;
-    const Cand* cands = in.cand + item * total;
-    const Slice* parts = in.slice + item * n_beams * slices;
+    const int groups = tiles * kTileGroups;
+    const int64_t first_beam = static_cast<int64_t>(blockIdx.x) * n_beams;
+    const Item<E> item{logits + first_beam * row_stride, row_stride, vocab, n_beams, groups, eos,
+                       in.top + first_beam * groups};
 
-    // the first kHold candidates of a thread stay in registers
-    Cand held[kHold];
+    // The largest logits of the groups, four at a time, or one where that leaves
+    // threads idle; a thread's first kHold stay in registers.
+    const int wide = n_beams * groups <= kMergeThreads * kHold ? 1 : 4;
+    const int per = groups / wide, total = n_beams * per;
+    const auto tops_of = [&](int i) {
+        if (wide == 4) return reinterpret_cast<const f32x4*>(item.tops)[i];
+        return f32x4{item.tops[i], -INFINITY, -INFINITY, -INFINITY};
+    };
+    f32x4 held[kHold];
     int beam[kHold];
 #pragma unroll
-    for (int c = 0; c < kHold; ++c) {
-        const int i = t + c * kMergeThreads;
-        beam[c] = i < total ? i / per : -1;
-        if (i < total) held[c] = cands[i];
+    for (int q = 0; q < kHold; ++q) {
+        const int i = t + q * kMergeThreads;
+        held[q] = f32x4{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        if (i < total) held[q] = tops_of(i);
     }
-
     // normalisers, `group` lanes per beam; scores and flags are read before anything is written
+#pragma unroll 1
     for (int w0 = 0; w0 < n_beams; w0 += kMergeThreads / group) {
         const int w = w0 + t / group, g = t % group;
         if (w >= n_beams) continue;
-        const float s = scores[item * n_beams + w];
-        const int st = !isfinite(s) ? kEmpty : finished && finished[item * n_beams + w] ? kFinished : kLive;
-        float ref = kLeastRef;
-        double sum = 0.0;
-        int found = 0;
-        if (st == kLive) {
-            for (int i = g; i < slices; i += group) {
-                const Slice q = parts[w * slices + i];
-                const float to = fmaxf(ref, q.ref);
-                sum = sum * static_cast<double>(__builtin_amdgcn_exp2f(ref - to)) +
-                      q.sum * static_cast<double>(__builtin_amdgcn_exp2f(q.ref - to));
-                ref = to;
-                found |= q.n;
-            }
-            float to = ref;
-            for (int o = group >> 1; o >= 1; o >>= 1) to = fmaxf(to, __shfl_xor(to, o));
-            sum *= static_cast<double>(__builtin_amdgcn_exp2f(ref - to));
+        const Slice* parts = in.slice + (first_beam + w) * slices;
+        Slice q{0.0, kLeastRef, 0};
+        if (g < slices) q = parts[g];  // not written if the beam is not live: not used then
+        const float score = scores[first_beam + w];
+        const bool ended = finished && finished[first_beam + w];
+        const int st = !isfinite(score) ? kEmpty : ended ? kFinished : kLive;
+        float ref = q.ref;
+        double sum = q.sum;
+#pragma unroll 1
+        for (int i = g + group; i < slices; i += group) {
+            q = parts[i];
+            const float to = fmaxf(ref, q.ref);
+            sum = sum * static_cast<double>(__builtin_amdgcn_exp2f(ref - to)) +
+                  q.sum * static_cast<double>(__builtin_amdgcn_exp2f(q.ref - to));
             ref = to;
-            for (int o = group >> 1; o >= 1; o >>= 1) {
-                sum += __shfl_xor(sum, o);
-                found |= __shfl_xor(found, o);
-            }
         }
+        float to = ref;
+#pragma unroll 1
+        for (int o = group >> 1; o >= 1; o >>= 1) to = fmaxf(to, __shfl_xor(to, o));
+        sum *= static_cast<double>(__builtin_amdgcn_exp2f(ref - to));
+#pragma unroll 1
+        for (int o = group >> 1; o >= 1; o >>= 1) sum += __shfl_xor(sum, o);
         if (g == 0) {
-            score[w] = s;
-            // a sum below 1/2 never reached its reference: all of the row lies below kLeastRef
-            const bool sound = sum > 0.5;
-            state[w] = st == kLive && found && !sound ? kRetake : st;
-            lse[w] = sound ? (static_cast<double>(ref) + log2(sum)) / static_cast<double>(kLog2e) : 0.0;
+            // a sum below 1/2 never reached its reference: all of the row lies below kLeastRef, or is excluded
+            const bool sound = st == kLive && sum > 0.5;
+            s.score[w] = score;
+            s.state[w] = st == kLive && !sound ? kRetake : st;
+            s.lse[w] = sound ? (static_cast<double>(to) + log2(sum)) / static_cast<double>(kLog2e) : 0.0;
+            s.set_shift(w);
         }
     }
-    __syncthreads();
-
-    const auto scored = [&](int i, int w, const Cand& x, Scored& c) {  // false: there is no such candidate
-        const int st = state[w];
-        if (st == kFinished) {
-            c = Scored{static_cast<double>(score[w]), 0.0f, w, eos};
-            return i == w * per;
-        }
-        c = Scored{score[w] + (static_cast<double>(x.z) - lse[w]), x.z, w, x.v};
-        return st != kEmpty && x.v >= 0;
-    };
-    const auto each = [&](auto&& f) {
-        Scored c;
 #pragma unroll
-        for (int q = 0; q < kHold; ++q)
-            if (beam[q] >= 0 && scored(t + q * kMergeThreads, beam[q], held[q], c)) f(c);
-        for (int i = t + kHold * kMergeThreads; i < total; i += kMergeThreads)
-            if (scored(i, i / per, cands[i], c)) f(c);
-    };
+    for (int q = 0; q < kHold; ++q) {
+        const int i = t + q * kMergeThreads;
+        beam[q] = i < total ? static_cast<int>(static_cast<unsigned int>(i) / static_cast<unsigned int>(per)) : 0;
+    }
+    const auto best_of = [](const f32x4& q) { return fmaxf(fmaxf(q[0], q[1]), fmaxf(q[2], q[3])); };
+    __syncthreads();
+    static_assert(kBeamMaxBeams <= 64, "a lane per beam");
+    if (__ballot(lane < n_beams && s.state[lane] == kRetake)) retake(s, item);
 
+    int m;
     // Every further round has taken at least one more row in float64.
     for (;;) {
-        for (int w = 0; w < n_beams; ++w) {
-            if (state[w] != kRetake) continue;
-            float m = -INFINITY;
-            for (int i = t; i < slices; i += kMergeThreads) {
-                const Cand c = cands[(w * slices + i) * k];
-                if (c.v >= 0) m = fmaxf(m, c.z);
-            }
+        // What k groups reach: each of the waves holds `share` lanes that reach the least
+        // of their bounds, or one wave holds k. z + shift is formed in float32 here; shift
+        // and sum are off by 2^-24 of themselves, which is taken off the bounds.
+        float mine = -INFINITY;
+        const auto look = [&](const f32x4& q, int w) {
+            const float shift = s.shift[w], sc = best_of(q) + shift;
+            mine = fmaxf(mine, sc - 0x1p-22f * (fabsf(sc) + fabsf(shift)));
+        };
 #pragma unroll
-            for (int o = 32; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
-            __syncthreads();
-            if (lane == 0) dred[wave] = m;
-            __syncthreads();
-            for (int q = 0; q < kW; ++q) m = fmaxf(m, static_cast<float>(dred[q]));
-            double sum = 0.0;
-            const E* p = logits + (item * n_beams + w) * row_stride;
-            for (int64_t i = t; i < vocab; i += kMergeThreads) {
-                const float z = widen(p[i]);
-                if (isfinite(z)) sum += exp(static_cast<double>(z) - m);
-            }
+        for (int q = 0; q < kHold; ++q) look(held[q], beam[q]);
+#pragma unroll 1
+        for (int i = t + kHold * kMergeThreads; i < total; i += kMergeThreads) look(tops_of(i), i / per);
+        const float2 reached = reached_by(mine, (k + kW - 1) / kW, k);
+        if (lane == 0) s.bound[wave][0] = reached.x, s.bound[wave][1] = reached.y;
+        if (t == 0) s.count = s.quad_count = s.near_count = s.again = 0;
+        __syncthreads();
+        float least_f = s.bound[0][0], alone = s.bound[0][1];
 #pragma unroll
-            for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o);
-            __syncthreads();
-            if (lane == 0) dred[wave] = sum;
-            __syncthreads();
-            if (t == 0) {
-                sum = 0.0;
-                for (int q = 0; q < kW; ++q) sum += dred[q];
-                lse[w] = m + log(sum);
-                state[w] = kExact;
+        for (int q = 1; q < kW; ++q) {
+            least_f = fminf(least_f, s.bound[q][0]);
+            alone = fmaxf(alone, s.bound[q][1]);
+        }
+        least_f = fmaxf(least_f, alone);
+        // the groups that may reach it, or come near it, by the same sums
+        const auto reach = [&](float shift) {
+            return least_f - 0x1p-22f * (fabsf(least_f) + fabsf(shift)) - 2.0f * static_cast<float>(tol);
+        };
+        const auto reaches = [&](const f32x4& q, int w) {
+            const float shift = s.shift[w], sc = best_of(q) + shift;
+            return sc > -INFINITY && sc >= reach(shift);
+        };
+        const auto take = [&](const f32x4& q, int i, int w) {
+            if (!reaches(q, w)) return;
+            const int at = atomicAdd(&s.quad_count, 1);
+            if (at >= kNear) return;
+            s.quad[at] = q;
+            s.quad_at[at] = int2{w, (i - w * per) * wide};
+        };
+#pragma unroll
+        for (int q = 0; q < kHold; ++q) take(held[q], t + q * kMergeThreads, beam[q]);
+#pragma unroll 1
+        for (int i = t + kHold * kMergeThreads; i < total; i += kMergeThreads) take(tops_of(i), i, i / per);
+        __syncthreads();
+        const int quads = s.quad_count;
+#pragma unroll 1
+        for (int i = t; i < min(quads, kNear) * 4; i += kMergeThreads) {
+            const float z = reinterpret_cast<const float*>(s.quad)[i];
+            const int2 q = s.quad_at[i >> 2];
+            const float shift = s.shift[q.x];
+            if (z > -INFINITY && z + shift >= reach(shift)) {
+                const int at = atomicAdd(&s.near_count, 1);
+                if (at < kNear) s.near[at] = int2{q.x, q.y + (i & 3)};
             }
         }
         __syncthreads();
-
-        // a score that k candidates reach, then the candidates near or above it
-        double mine = -INFINITY;
-        each([&](const Scored& c) { mine = fmax(mine, c.s); });
-        const unsigned int o = mine > -INFINITY ? order_hi(mine) : 0;
-        unsigned int b = 0;
+        const int near = s.near_count;
+        bool fits = quads <= kNear && near <= kNear;
+        if (fits) {
+            // their elements
+#pragma unroll 1
+            for (int i = t; i < near * kGroupChunks; i += kMergeThreads) {
+                const int2 g = s.near[i / kGroupChunks];
+                const Row<E> row = item.row(g.x);
+                const int64_t c = int64_t{g.y} * kGroupChunks + i % kGroupChunks;
+                if (c >= row.chunks) continue;
+                const u32x4 x = reinterpret_cast<const u32x4*>(row.p + row.head)[c];
+                const float shift = s.shift[g.x], from = reach(shift);
+                const int v = row.head + static_cast<int>(c) * kPer;
 #pragma unroll
-        for (int bit = 31; bit >= 8; --bit) {
-            const unsigned int c = b | (1u << bit);
-            if (__popcll(__ballot(o >= c)) >= k) b = c;
-        }
-        if (lane == 0) bound[wave] = b;
-        if (t == 0) count = again = 0;
-        __syncthreads();
-        b = 0;
-#pragma unroll
-        for (int q = 0; q < kW; ++q) b = bound[q] > b ? bound[q] : b;
-        const double least = b ? value_hi(b) - tol : -INFINITY;
-        each([&](const Scored& c) {
-            if (c.s >= least) {
-                const int at = atomicAdd(&count, 1);
-                if (at < kMergeList) list[at] = c;
-            }
-        });
-        __syncthreads();
-        const int n = count;
-        const int m = n < k + 1 ? n : k + 1;
-        if (n <= kMergeList) {
-            for (int i0 = 0; i0 < n; i0 += kMergeThreads / 4) {  // four lanes per candidate
-                const int i = i0 + (t >> 2);
-                int rank = 0;
-                Scored c{};
-                if (i < n) {
-                    c = list[i];
-                    for (int j = t & 3; j < n; j += 4) rank += before(list[j], c);
+                for (int e = 0; e < kPer; ++e) {
+                    const float z = Elem<E>::get(x, e);
+                    if (z + shift >= from && isfinite(z)) s.add(s.scored(z, g.x, v + e));
                 }
-                rank += __shfl_xor(rank, 1);
-                rank += __shfl_xor(rank, 2);
-                if (i < n && (t & 3) == 0 && rank < m) ranked[rank] = c;
             }
-        } else {
-            // too many near one another (long ties): one after the other
-            const Scored none{-INFINITY, -INFINITY, 0x7fffffff, 0x7fffffff};
-            for (int j = 0; j < m; ++j) {
-                Scored best = none;
-                each([&](const Scored& c) {
-                    if ((j == 0 || before(ranked[j - 1], c)) && before(c, best)) best = c;
+            if (loose)
+                item.each_loose(s, [&](const Scored& c) {
+                    if (static_cast<float>(c.s) >= reach(s.shift[c.w])) s.add(c);
                 });
-#pragma unroll
-                for (int d = 32; d >= 1; d >>= 1) {
-                    const Scored other{__shfl_xor(best.s, d), __shfl_xor(best.z, d), __shfl_xor(best.w, d),
-                                       __shfl_xor(best.v, d)};
-                    if (before(other, best)) best = other;
-                }
-                if (lane == 0) pick[wave] = best;
-                __syncthreads();
-                if (t == 0) {
-                    for (int q = 1; q < kW; ++q)
-                        if (before(pick[q], best)) best = pick[q];
-                    ranked[j] = best;
-                }
-                __syncthreads();
+            else if (t < n_beams && s.state[t] == kFinished)
+                s.add(Scored{static_cast<double>(s.score[t]), 0.0f, t, eos});
+            __syncthreads();
+            const int n = s.count;
+            fits = n <= kMergeList;
+            m = n < k + 1 ? n : k + 1;
+            if (fits) s.rank(n, m);
+            __syncthreads();
+        }
+        if (!fits) m = pick_slowly(s, item, k + 1);
+        if (t + 1 < m) {
+            const Scored x = s.ranked[t], y = s.ranked[t + 1];
+            if (x.w != y.w && x.s - y.s <= tol) {
+                if (s.state[x.w] == kLive) s.state[x.w] = kRetake, s.again = 1;
+                if (s.state[y.w] == kLive) s.state[y.w] = kRetake, s.again = 1;
             }
         }
         __syncthreads();
-        if (t + 1 < m && ranked[t].w != ranked[t + 1].w && ranked[t].s - ranked[t + 1].s <= tol)
-            for (int q = 0; q < 2; ++q)
-                if (state[ranked[t + q].w] == kLive) {
-                    state[ranked[t + q].w] = kRetake;
-                    again = 1;
-                }
-        __syncthreads();
-        if (!again) break;
+        if (!s.again) break;
+        retake(s, item);
     }
 
     if (t < k) {
-        const int64_t at = item * k + t;
-        const bool some = t < count;
-        const Scored c = ranked[some ? t : 0];
+        const int64_t at = static_cast<int64_t>(blockIdx.x) * k + t;
+        const bool some = t < m;
+        const Scored c = s.ranked[some ? t : 0];
         scores_out[at] = some ? static_cast<float>(c.s) : -INFINITY;
         parents_out[at] = some ? c.w : -1;
         tokens_out[at] = some ? c.v : -1;
-        finished_out[at] = some && (state[c.w] == kFinished || c.v == eos);
+        finished_out[at] = some && (s.state[c.w] == kFinished || c.v == eos);
     }
 }
 
 struct Shape {
-    int slices;
+    int tiles;  // of every row, also of one that begins inside a chunk
     int tiles_per_slice;
+    int slices;
 };
 
-// Slices of a row: enough waves to fill the chip, none shorter than a tile.
+// Slices of a row: enough waves to fill the chip, none with less than a tile.
 Shape shape_of(int type, int64_t vocab, int64_t rows) {
-    const int64_t per_tile = int64_t{64} * kChunks * (type == kBF16 ? 8 : 4);
-    const int64_t tiles = (vocab + 15) / per_tile + 1;  // a row that starts inside a chunk may touch one tile more
-    int64_t slices = (4096 + rows - 1) / rows;
+    const int64_t per_tile = int64_t{kTile} * (type == kBF16 ? 8 : 4);
+    const int64_t tiles = (vocab + per_tile - 1) / per_tile;
+    int64_t slices = (kTargetWaves + rows - 1) / rows;
     if (slices > tiles) slices = tiles;
     const int64_t per = (tiles + slices - 1) / slices;
-    return Shape{static_cast<int>((tiles + per - 1) / per), static_cast<int>(per)};
+    return Shape{static_cast<int>(tiles), static_cast<int>(per), static_cast<int>((tiles + per - 1) / per)};
 }
 
 int64_t align16(int64_t b) { return (b + 15) & ~int64_t{15}; }
@@ -556,14 +634,12 @@ hipError_t launch_typed(const BeamArgs& a, void* workspace, hipStream_t stream) 
     const Shape sh = shape_of(a.type, a.vocab, rows);
     Layout lay;
     lay.slice = static_cast<Slice*>(workspace);
-    lay.cand = reinterpret_cast<Cand*>(static_cast<char*>(workspace) +
+    lay.top = reinterpret_cast<float*>(static_cast<char*>(workspace) +
                                        align16(rows * sh.slices * static_cast<int64_t>(sizeof(Slice))));
     const E* logits = static_cast<const E*>(a.logits);
-    const int drop_at = a.n_select * 2 > 32 ? a.n_select * 2 : 32;
     const int64_t blocks = (rows * sh.slices + kWaves - 1) / kWaves;
     beam_scan_kernel<E><<<dim3(static_cast<unsigned>(blocks)), kWaves * 64, 0, stream>>>(
-        logits, a.vocab, a.row_stride, rows, sh.slices, sh.tiles_per_slice, a.n_select, drop_at, a.scores, a.finished,
-        lay);
+        logits, a.vocab, a.row_stride, rows, sh.slices, sh.tiles, sh.tiles_per_slice, a.scores, a.finished, lay);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     // Twice what a float32 normaliser may be off, in nats: the exponentials'
@@ -572,22 +648,25 @@ hipError_t launch_typed(const BeamArgs& a, void* workspace, hipStream_t stream) 
     // a sum of 8 and 2 more additions by 2^-24 each, log2 e by 2^-26 of the
     // entropy.
     const double tol = 2.0 * 0x1p-24 * (24.0 + log2(static_cast<double>(a.vocab)));
+    // whether a row may have elements outside its chunks
+    constexpr int kPer = Elem<E>::kPer;
+    const int loose = reinterpret_cast<uintptr_t>(logits) % 16 != 0 || a.row_stride % kPer != 0 || a.vocab % kPer != 0;
     int group = 1;  // lanes that join one beam's slices
     while (group < sh.slices && group < 64) group *= 2;
     beam_merge_kernel<E><<<dim3(static_cast<unsigned>(a.n_items)), kMergeThreads, 0, stream>>>(
-        logits, a.vocab, a.row_stride, a.n_beams, sh.slices, group, a.n_select, tol, a.scores, a.finished, a.eos, lay,
-        a.scores_out, a.parents_out, a.tokens_out, a.finished_out);
+        logits, a.vocab, a.row_stride, a.n_beams, sh.slices, group, sh.tiles, loose, a.n_select, tol, a.scores, a.finished,
+        a.eos, lay, a.scores_out, a.parents_out, a.tokens_out, a.finished_out);
     return hipGetLastError();
 }
 
 }  // namespace
 
-int64_t beam_workspace_bytes(int type, int64_t vocab, int64_t n_items, int n_beams, int n_select) {
+int64_t beam_workspace_bytes(int type, int64_t vocab, int64_t n_items, int n_beams, int) {
     const int64_t rows = n_items * n_beams;
     if (rows == 0) return 0;
     const Shape sh = shape_of(type, vocab, rows);
     return align16(rows * sh.slices * static_cast<int64_t>(sizeof(Slice))) +
-           rows * sh.slices * n_select * static_cast<int64_t>(sizeof(Cand));
+           rows * sh.tiles * kTileGroups * static_cast<int64_t>(sizeof(float));
 }
 
 hipError_t launch_beam_select(const BeamArgs& a, void* workspace, hipStream_t stream) {
