@@ -222,7 +222,7 @@ __device__ __forceinline__ bool before(const Scored& a, const Scored& b) {
 }
 
 __device__ __forceinline__ unsigned int order_of(float z) {
-    const unsigned int u = __float_as_uint(z);
+    const unsigned int u = __float_as_uint(z + 0.0f);  // -0 and 0 are alike
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 __device__ __forceinline__ float value_of(unsigned int o) {
@@ -244,6 +244,15 @@ __device__ __forceinline__ float2 reached_by(float x, int few, int many) {
 
 enum : int { kEmpty, kLive, kFinished, kRetake, kExact };  // kRetake: live, its normaliser is to be taken in float64
 
+// log2 of a positive normal number, off by less than 3 x 2^-24: its exponent, and
+// the float32 logarithm of its mantissa in [1, 2).
+__device__ __forceinline__ double log2_of(double x) {
+    const uint64_t u = static_cast<uint64_t>(__double_as_longlong(x));
+    const double mantissa = __longlong_as_double(static_cast<long long>((u & 0xfffffffffffffull) | 0x3ff0000000000000ull));
+    return static_cast<double>(static_cast<int>(u >> 52) - 1023) +
+           static_cast<double>(__builtin_amdgcn_logf(static_cast<float>(mantissa)));
+}
+
 struct Merge {
     float score[kBeamMaxBeams];
     double lse[kBeamMaxBeams];
@@ -253,8 +262,8 @@ struct Merge {
     int2 quad_at[kNear];         // their beams and first groups
     int2 near[kNear];            // those groups: beam, place
     double list_s[kMergeList];   // candidates: score,
-    float list_z[kMergeList];    // logit,
-    int2 list_wv[kMergeList];    // beam and id
+    uint64_t list_k[kMergeList]; // beam and logit, the first of equal scores with the least,
+    int list_v[kMergeList];      // id
     Scored ranked[kBeamMaxSelect + 1];
     Scored pick[kMergeThreads / 64];
     double part[kMergeThreads / 64];
@@ -271,31 +280,31 @@ struct Merge {
         const int at = atomicAdd(&count, 1);
         if (at >= kMergeList) return;
         list_s[at] = c.s;
-        list_z[at] = c.z;
-        list_wv[at] = int2{c.w, c.v};
+        list_k[at] = (static_cast<uint64_t>(c.w) << 32) | ~order_of(c.z);
+        list_v[at] = c.v;
     }
-    __device__ __forceinline__ Scored listed(int i) const {
-        return Scored{list_s[i], list_z[i], list_wv[i].x, list_wv[i].y};
-    }
-    // The list's first m entries in order; four lanes per entry.
+    // The list's first m entries in order; four lanes per entry count the ones
+    // before it, without a branch: equal logits of one beam are common.
     __device__ __forceinline__ void rank(int n, int m) {
         const int t = threadIdx.x;
 #pragma unroll 1
         for (int i0 = 0; i0 < n; i0 += kMergeThreads / 4) {
-            const int i = i0 + (t >> 2);
+            const int i = i0 + (t >> 2), q = i < n ? i : 0;
+            const double s = list_s[q];
+            const uint64_t k = list_k[q];
+            const int v = list_v[q];
             int at = 0;
-            Scored c{};
-            if (i < n) {
-                c = listed(i);
 #pragma unroll 4
-                for (int j = t & 3; j < n; j += 4) {
-                    const double other = list_s[j];
-                    at += other > c.s || (other == c.s && before(listed(j), c));
-                }
+            for (int j = t & 3; j < n; j += 4) {
+                const double os = list_s[j];
+                const uint64_t ok = list_k[j];
+                const int ov = list_v[j];
+                at += (os > s) | ((os == s) & ((ok < k) | ((ok == k) & (ov < v))));
             }
             at += __shfl_xor(at, 1);
             at += __shfl_xor(at, 2);
-            if (i < n && (t & 3) == 0 && at < m) ranked[at] = c;
+            if (i < n && (t & 3) == 0 && at < m)
+                ranked[at] = Scored{s, value_of(~static_cast<unsigned int>(k)), static_cast<int>(k >> 32), v};
         }
     }
 };
@@ -482,7 +491,7 @@ __global__ void __launch_bounds__(kMergeThreads)
             const bool sound = st == kLive && sum > 0.5;
             s.score[w] = score;
             s.state[w] = st == kLive && !sound ? kRetake : st;
-            s.lse[w] = sound ? (static_cast<double>(to) + log2(sum)) / static_cast<double>(kLog2e) : 0.0;
+            s.lse[w] = sound ? (static_cast<double>(to) + log2_of(sum)) / static_cast<double>(kLog2e) : 0.0;
             s.set_shift(w);
         }
     }
@@ -508,7 +517,10 @@ __global__ void __launch_bounds__(kMergeThreads)
             mine = fmaxf(mine, sc - 0x1p-22f * (fabsf(sc) + fabsf(shift)));
         };
 #pragma unroll
-        for (int q = 0; q < kHold; ++q) look(held[q], beam[q]);
+        for (int q = 0; q < kHold; ++q) {
+            if (q * kMergeThreads >= total) break;
+            look(held[q], beam[q]);
+        }
 #pragma unroll 1
         for (int i = t + kHold * kMergeThreads; i < total; i += kMergeThreads) look(tops_of(i), i / per);
         const float2 reached = reached_by(mine, (k + kW - 1) / kW, k);
@@ -538,7 +550,10 @@ __global__ void __launch_bounds__(kMergeThreads)
             s.quad_at[at] = int2{w, (i - w * per) * wide};
         };
 #pragma unroll
-        for (int q = 0; q < kHold; ++q) take(held[q], t + q * kMergeThreads, beam[q]);
+        for (int q = 0; q < kHold; ++q) {
+            if (q * kMergeThreads >= total) break;
+            take(held[q], t + q * kMergeThreads, beam[q]);
+        }
 #pragma unroll 1
         for (int i = t + kHold * kMergeThreads; i < total; i += kMergeThreads) take(tops_of(i), i, i / per);
         __syncthreads();
@@ -567,10 +582,14 @@ __global__ void __launch_bounds__(kMergeThreads)
                 const u32x4 x = reinterpret_cast<const u32x4*>(row.p + row.head)[c];
                 const float shift = s.shift[g.x], from = reach(shift);
                 const int v = row.head + static_cast<int>(c) * kPer;
+#pragma unroll 1
+                for (int j = 0; j < 4; ++j) {
+                    const unsigned int word = j < 2 ? (j == 0 ? x[0] : x[1]) : (j == 2 ? x[2] : x[3]);
 #pragma unroll
-                for (int e = 0; e < kPer; ++e) {
-                    const float z = Elem<E>::get(x, e);
-                    if (z + shift >= from && isfinite(z)) s.add(s.scored(z, g.x, v + e));
+                    for (int e = 0; e < kPer / 4; ++e) {
+                        const float z = Elem<E>::get(u32x4{word, 0, 0, 0}, e);
+                        if (z + shift >= from && isfinite(z)) s.add(s.scored(z, g.x, v + j * (kPer / 4) + e));
+                    }
                 }
             }
             if (loose)
