@@ -472,8 +472,8 @@ kld_status kld_eval_compare_noalloc(const void* base, const void* quant, int64_t
  * infinity) are excluded tokens: they add nothing to the normaliser and are
  * never chosen. A live beam offers every other token v at
  * s_w + z_v - log(sum exp z); a finished beam offers only itself, as token
- * eos_token at s_w, and its logits are not read; a beam whose score is not
- * finite is empty and offers nothing. The n_select best of all beams together
+ * eos_token at s_w, whatever its logits are; a beam whose score is not finite
+ * is empty and offers nothing. The n_select best of all beams together
  * are chosen, best first, equal scores by lowest beam, then lowest id. Scores
  * are compared as in float64 (one beam's candidates by their logits).
  *   logits       device rows of `vocab` elements of `dtype`, row_stride

@@ -431,7 +431,7 @@ __device__ __attribute__((noinline)) int pick_slowly(Merge& s, const Item<E>& it
 template <class E>
 __global__ void __launch_bounds__(kMergeThreads)
     beam_merge_kernel(const E* __restrict__ logits, int64_t vocab, int64_t row_stride, int n_beams, int slices,
-                      int group, int tiles, int loose, int k, double tol, const float* scores, const uint8_t* finished, int eos,
+                      int group, int tiles, int loose, int64_t first_item, int k, double tol, const float* scores, const uint8_t* finished, int eos,
                       Layout in, float* scores_out, int32_t* __restrict__ parents_out,
                       int32_t* __restrict__ tokens_out, uint8_t* finished_out) {
     constexpr int kW = kMergeThreads / 64;
@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(kMergeThreads)
     __shared__ Merge s;
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     const int groups = tiles * kTileGroups;
-    const int64_t first_beam = static_cast<int64_t>(blockIdx.x) * n_beams;
+    const int64_t this_item = first_item + blockIdx.x, first_beam = this_item * n_beams;
     const Item<E> item{logits + first_beam * row_stride, row_stride, vocab, n_beams, groups, eos,
                        in.top + first_beam * groups};
 
@@ -619,7 +619,7 @@ __global__ void __launch_bounds__(kMergeThreads)
     }
 
     if (t < k) {
-        const int64_t at = static_cast<int64_t>(blockIdx.x) * k + t;
+        const int64_t at = this_item * k + t;
         const bool some = t < m;
         const Scored c = s.ranked[some ? t : 0];
         scores_out[at] = some ? static_cast<float>(c.s) : -INFINITY;
@@ -672,10 +672,16 @@ hipError_t launch_typed(const BeamArgs& a, void* workspace, hipStream_t stream) 
     const int loose = reinterpret_cast<uintptr_t>(logits) % 16 != 0 || a.row_stride % kPer != 0 || a.vocab % kPer != 0;
     int group = 1;  // lanes that join one beam's slices
     while (group < sh.slices && group < 64) group *= 2;
-    beam_merge_kernel<E><<<dim3(static_cast<unsigned>(a.n_items)), kMergeThreads, 0, stream>>>(
-        logits, a.vocab, a.row_stride, a.n_beams, sh.slices, group, sh.tiles, loose, a.n_select, tol, a.scores, a.finished,
-        a.eos, lay, a.scores_out, a.parents_out, a.tokens_out, a.finished_out);
-    return hipGetLastError();
+    const int64_t per = max_blocks_per_launch(kMergeThreads);
+    for (int64_t first = 0; first < a.n_items; first += per) {
+        const int64_t n = a.n_items - first < per ? a.n_items - first : per;
+        beam_merge_kernel<E><<<dim3(static_cast<unsigned>(n)), kMergeThreads, 0, stream>>>(
+            logits, a.vocab, a.row_stride, a.n_beams, sh.slices, group, sh.tiles, loose, first, a.n_select, tol,
+            a.scores, a.finished, a.eos, lay, a.scores_out, a.parents_out, a.tokens_out, a.finished_out);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace

@@ -495,7 +495,8 @@ __global__ void __launch_bounds__(kThreads) run_sum_kernel(GradIn<EG, EO> a, Gra
     const int words = lane <= n ? g.word[i0 + lane] : -1;
     const int perms = lane < n ? g.perm[i0 + lane] : 0;
     bool entered = i0 > 0 && g.word[i0 - 1] == __builtin_amdgcn_readlane(words, 0);
-    if (col >= a.dim) return;
+    // lanes past the row's end stay: the others read their positions
+    const bool mine = col < a.dim;
     const int64_t wide = (a.dim + 3) & ~int64_t{3};
     const EG* from = a.grad + col;
     float acc[V] = {};
@@ -503,10 +504,12 @@ __global__ void __launch_bounds__(kThreads) run_sum_kernel(GradIn<EG, EO> a, Gra
     for (int i = 0; i < n; i += kAhead) {
         Vec<EG, V> row[kAhead];
 #pragma unroll
-        for (int q = 0; q < kAhead; ++q)
-            if (i + q < n)
-                row[q] = *reinterpret_cast<const Vec<EG, V>*>(
-                    from + __builtin_amdgcn_readlane(perms, i + q) * a.grad_stride);
+        for (int q = 0; q < kAhead; ++q) {
+            if (i + q >= n) break;
+            const int64_t at_row = __builtin_amdgcn_readlane(perms, i + q) * a.grad_stride;
+            row[q] = Vec<EG, V>{};
+            if (mine) row[q] = *reinterpret_cast<const Vec<EG, V>*>(from + at_row);
+        }
 #pragma unroll
         for (int q = 0; q < kAhead; ++q) {
             if (i + q >= n) break;
@@ -515,7 +518,8 @@ __global__ void __launch_bounds__(kThreads) run_sum_kernel(GradIn<EG, EO> a, Gra
             const int word = __builtin_amdgcn_readlane(words, i + q);
             const bool ends = __builtin_amdgcn_readlane(words, i + q + 1) != word;
             if (!ends && i + q + 1 < n) continue;
-            if (ends && !entered) {
+            if (!mine) {
+            } else if (ends && !entered) {
                 finish<EG, EO, V>(a, word, col, acc);
             } else {
                 float* to = g.part + (int64_t{piece} * 2 + (entered ? 0 : 1)) * wide + col;

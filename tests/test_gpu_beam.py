@@ -263,6 +263,33 @@ def test_captured_and_replayed():
             assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_as_many_items_as_a_call_takes(dtype):
+    """2^22 items of one beam: more workgroups than one launch may have."""
+    items, vocab = 1 << 22, 8
+    g = torch.Generator(device=DEV).manual_seed(1)
+    z = torch.randn(items, vocab, generator=g, device=DEV).to(TYPES[dtype])
+    s, p, t, f = qqe.beam_select(z, torch.zeros(items, 1, device=DEV), 2)
+    logp = torch.log_softmax(z.double(), 1)
+    top = z.float().max(1)
+    assert torch.equal(t[:, 0].long(), top.indices) and not p.any() and not f.any()
+    assert ((s[:, 0].double() - logp.gather(1, top.indices[:, None])[:, 0]).abs() <= 2.0 ** -24 * 8 + norm_tol(vocab)).all()
+    with pytest.raises(qqe.KldEvalError, match="4194304"):
+        qqe.beam_select(torch.zeros(items + 1, 1, device=DEV), torch.zeros(items + 1, 1, device=DEV))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("items,beams,k,vocab", [(2, 12, 24, 151936), (1, 64, 8, 32000), (1, 16, 64, 262144),
+                                                 (2, 1, 64, 5000), (3, 2, 2, 600000)])
+def test_many_groups(items, beams, k, vocab, dtype):
+    """More group maxima than a workgroup keeps in registers, and few of them
+    for a large k."""
+    z, scores, g = make(items, beams, vocab, dtype, seed=21)
+    run_and_check(z, scores, k, eos=3, ctx="many groups")
+    z[:, vocab // 3:] = float("-inf")
+    run_and_check(z, scores, k, eos=3, ctx="many groups, masked")
+
+
 def test_refusals_with_device_tensors():
     z, scores, _ = make(2, 3, 100, "f32")
     ok = dict(dtype=torch.float32, device=DEV)
