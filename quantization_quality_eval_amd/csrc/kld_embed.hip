@@ -100,24 +100,40 @@ constexpr int widest() {
 
 // ---- lookup ----
 
-template <class ET, class EO, int V>
+constexpr int kRows = 4;              // rows a thread of a large lookup takes
+constexpr int64_t kFullWaves = 8192;  // what a large lookup leaves at least
+
+// R consecutive positions per row unit, their rows in flight together.
+template <class ET, class EO, int V, int R>
 __global__ void __launch_bounds__(kThreads)
     embed_kernel(const ET* __restrict__ table, int64_t vocab, int64_t dim, int64_t table_stride,
                  const int32_t* __restrict__ tokens, int64_t n_tokens, double scale, EO* __restrict__ out,
                  int64_t out_stride, Cover c) {
     const Place at = place_of<V>(c);
-    if (at.unit >= n_tokens || at.col >= dim) return;
-    const int32_t t = tokens[at.unit];
-    Vec<EO, V> o;
-    if (t >= 0 && t < vocab) {
-        const Vec<ET, V> x = *reinterpret_cast<const Vec<ET, V>*>(table + t * table_stride + at.col);
+    const int64_t n0 = at.unit * R;
+    if (n0 >= n_tokens || at.col >= dim) return;
+    int32_t t[R];
+    Vec<ET, V> x[R];
 #pragma unroll
-        for (int e = 0; e < V; ++e) put(&o.x[e], static_cast<float>(static_cast<double>(widen(x.x[e])) * scale));
-    } else {
+    for (int q = 0; q < R; ++q) t[q] = n0 + q < n_tokens ? tokens[n0 + q] : -1;
 #pragma unroll
-        for (int e = 0; e < V; ++e) put(&o.x[e], t < 0 ? 0.0f : NAN);
+    for (int q = 0; q < R; ++q)
+        if (t[q] >= 0 && t[q] < vocab)
+            x[q] = *reinterpret_cast<const Vec<ET, V>*>(table + t[q] * table_stride + at.col);
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+        if (n0 + q >= n_tokens) break;
+        Vec<EO, V> o;
+        if (t[q] >= 0 && t[q] < vocab) {
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                put(&o.x[e], static_cast<float>(static_cast<double>(widen(x[q].x[e])) * scale));
+        } else {
+#pragma unroll
+            for (int e = 0; e < V; ++e) put(&o.x[e], t[q] < 0 ? 0.0f : NAN);
+        }
+        *reinterpret_cast<Vec<EO, V>*>(out + (n0 + q) * out_stride + at.col) = o;
     }
-    *reinterpret_cast<Vec<EO, V>*>(out + at.unit * out_stride + at.col) = o;
 }
 
 // ---- gradient ----
@@ -608,11 +624,18 @@ hipError_t embed_typed(const void* table, int64_t vocab, int64_t dim, int64_t ta
                        int64_t n_tokens, double scale, void* out, int64_t out_stride, hipStream_t s) {
     const auto run = [&](auto v) {
         constexpr int V = decltype(v)::value;
-        return launch_cover(cover_of<V>(dim), n_tokens, [&](const Cover& c, dim3 blocks) {
-            embed_kernel<ET, EO, V><<<blocks, kThreads, 0, s>>>(static_cast<const ET*>(table), vocab, dim, table_stride,
-                                                               tokens, n_tokens, scale, static_cast<EO*>(out),
-                                                               out_stride, c);
-        });
+        const Cover c = cover_of<V>(dim);
+        // several rows per thread once that leaves waves enough to fill the chip
+        const auto with = [&](auto r) {
+            constexpr int R = decltype(r)::value;
+            return launch_cover(c, (n_tokens + R - 1) / R, [&](const Cover& part, dim3 blocks) {
+                embed_kernel<ET, EO, V, R><<<blocks, kThreads, 0, s>>>(
+                    static_cast<const ET*>(table), vocab, dim, table_stride, tokens, n_tokens, scale,
+                    static_cast<EO*>(out), out_stride, part);
+            });
+        };
+        if (n_tokens / kRows * c.tiles * (c.lanes / 64) >= kFullWaves) return with(std::integral_constant<int, kRows>{});
+        return with(std::integral_constant<int, 1>{});
     };
     const auto both = [&](int v) {
         return allows(v, dim, table, table_stride, sizeof(ET)) && allows(v, dim, out, out_stride, sizeof(EO));
