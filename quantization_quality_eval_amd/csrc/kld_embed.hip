@@ -393,6 +393,7 @@ __global__ void __launch_bounds__(kThreads) bucket_group_kernel(GradSpace g, int
     __syncthreads();
     const int part = ((n + kW - 1) / kW + 63) & ~63;
     const int a = wave * part < n ? wave * part : n, b = a + part < n ? a + part : n;
+#pragma unroll 4
     for (int i = a + lane; i < b; i += 64) atomicAdd(&place[wave][g.bword[i0 + i] >> kLgBuckets], 1);
     __syncthreads();
     if (wave == 0) {
@@ -418,20 +419,31 @@ __global__ void __launch_bounds__(kThreads) bucket_group_kernel(GradSpace g, int
         }
     }
     __syncthreads();
-    for (int i = a; i < b; i += 64) {
-        const bool ok = i + lane < b;
-        const int x = ok ? g.bword[i0 + i + lane] : 0;
-        const int key = x >> kLgBuckets;
-        const unsigned long long same = same_key(__ballot(ok), key, id_bits);
-        const int first = ok ? place[wave][key] : 0;
-        __builtin_amdgcn_wave_barrier();
-        if (ok) {
-            const int to = first + __popcll(same & ((1ull << lane) - 1));
-            g.perm[to] = g.bperm[i0 + i + lane];
-            g.word[to] = x;
-            if (same >> lane == 1) place[wave][key] = to + 1;
+    constexpr int kTake = 4;  // loads in flight
+    for (int i1 = a; i1 < b; i1 += 64 * kTake) {
+        int x[kTake], n_of[kTake];
+#pragma unroll
+        for (int q = 0; q < kTake; ++q) {
+            const int i = i1 + q * 64 + lane;
+            x[q] = i < b ? g.bword[i0 + i] : -1;
+            n_of[q] = i < b ? g.bperm[i0 + i] : 0;
         }
-        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int q = 0; q < kTake; ++q) {
+            const bool ok = x[q] >= 0;
+            if (!__ballot(ok)) break;
+            const int key = x[q] >> kLgBuckets;
+            const unsigned long long same = same_key(__ballot(ok), key, id_bits);
+            const int first = ok ? place[wave][key] : 0;
+            __builtin_amdgcn_wave_barrier();
+            if (ok) {
+                const int to = first + __popcll(same & ((1ull << lane) - 1));
+                g.perm[to] = n_of[q];
+                g.word[to] = x[q];
+                if (same >> lane == 1) place[wave][key] = to + 1;
+            }
+            __builtin_amdgcn_wave_barrier();
+        }
     }
 }
 
