@@ -17,6 +17,14 @@
 //      kept in float32. Further workgroups of the launch set the rows that no
 //      position names to zero.
 //   3. join: the parts of each run that was cut, in order.
+//
+// Measured on MI355X. Lookup of 16384 rows of 151936 x 2048 bfloat16 into float32: 33
+// us for 164 MB (5.0 TB/s; one row per thread instead of four: 49). Gradient of 16384
+// positions x 4096 bfloat16 into a bfloat16 table of 32000: 100 us in all, of which
+// the sort takes 17, the sum and the zeros 74 (396 MB at 5.3 TB/s) and the join 9; of
+// 65536 positions x 256 into float32 x 151936: 69 us (sort 25, sum 27, join 8); of 100
+// positions: 12 us in three launches. Large sums are bound by memory, small ones by
+// the launches, which depend on one another.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -138,10 +146,13 @@ __global__ void __launch_bounds__(kThreads)
 
 // ---- gradient ----
 
-constexpr int kMostPiece = 32;   // positions per piece of the sum: this many where there are
-constexpr int kLeastPiece = 8;   // waves enough, down to this many where there are not
+// Positions per piece of the sum: 32 where that makes waves enough to fill the
+// chip, down to 8 where it does not (adding 8192 x 1000 float32: 20 us with 32, 15
+// with 16, 14 with 8; 16384 x 4096 bfloat16: the join takes 9 us with 32, 12 with 16).
+constexpr int kMostPiece = 32;
+constexpr int kLeastPiece = 8;
 constexpr int64_t kPieceWaves = 4096;
-constexpr int kAhead = 8;     // rows in flight per thread
+constexpr int kAhead = 8;     // rows in flight per thread; 16 cost registers (85 -> 107 us, 16384 x 4096)
 constexpr int kZeroRows = 8;  // rows of the table that a thread zeroes
 static_assert(kMostPiece < 64, "a lane per position and one more");
 
@@ -152,7 +163,9 @@ constexpr int kBucketIds = 1024;      // ids of one bucket at most
 constexpr int kSortThreads = 1024;
 constexpr int kMostChunks = 32;       // workgroups of its first two launches
 constexpr int64_t kChunkTokens = 1024;  // positions of one of them at least
-constexpr int64_t kFewTokens = 2048;    // up to here every wave reads every id
+// Up to here every wave reads every id: 12 us in all for 256 positions against 17
+// sorted, 16 and 18 for 1024, 22 and 19 for 2048.
+constexpr int64_t kFewTokens = 1536;
 
 struct GradSpace {
     int32_t* total;    // positions with a valid id
@@ -476,7 +489,25 @@ struct GradIn {
     int64_t out_stride;
     int64_t vocab;
     bool accumulate;
+    bool past_cache;
 };
+
+// V zeros; non-temporal where table and gradient together do not fit the
+// memory-side cache: a bfloat16 table of 262 MB and 134 MB of gradient take 100 us
+// so, 109 otherwise, while two micro-batches of 33 MB into a float32 table of 128 MB
+// take 96 and 90 us: there the second finds the first's rows in the cache.
+constexpr int64_t kCacheBytes = int64_t{256} << 20;
+template <class E, int V>
+__device__ __forceinline__ void zero(E* p, bool past_cache) {
+    if constexpr (V * sizeof(E) == 16) {
+        typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+        if (past_cache) {
+            __builtin_nontemporal_store(u32x4{0u, 0u, 0u, 0u}, reinterpret_cast<u32x4*>(p));
+            return;
+        }
+    }
+    *reinterpret_cast<Vec<E, V>*>(p) = Vec<E, V>{};
+}
 
 // A finished sum into its row: scaled in float64, added to what is there when
 // accumulating, rounded once.
@@ -512,7 +543,7 @@ __global__ void __launch_bounds__(kThreads) run_sum_kernel(GradIn<EG, EO> a, Gra
         }
 #pragma unroll
         for (int q = 0; q < kZeroRows; ++q)
-            if (named[q] == 0) *reinterpret_cast<Vec<EO, V>*>(a.out + (v0 + q) * a.out_stride + col) = Vec<EO, V>{};
+            if (named[q] == 0) zero<EO, V>(a.out + (v0 + q) * a.out_stride + col, a.past_cache);
         return;
     }
     // lane l holds the piece's l-th position and its id; lane n the id behind the piece
@@ -605,7 +636,9 @@ __global__ void __launch_bounds__(kThreads) run_join_kernel(GradIn<EG, EO> a, Gr
 template <class EG, class EO, int V>
 hipError_t grad_vec(const EmbedGradArgs& a, const GradSpace& g, hipStream_t s) {
     const GradIn<EG, EO> in{static_cast<const EG*>(a.grad), a.grad_stride, a.dim,   a.scale,
-                            static_cast<EO*>(a.out),        a.out_stride,  a.vocab, a.accumulate};
+                            static_cast<EO*>(a.out),        a.out_stride,  a.vocab, a.accumulate,
+                            a.vocab * a.dim * static_cast<int64_t>(sizeof(EO)) +
+                                    a.n_tokens * a.dim * static_cast<int64_t>(sizeof(EG)) > kCacheBytes};
     const int64_t zero_units = a.accumulate ? 0 : (a.vocab + kZeroRows - 1) / kZeroRows;
     const hipError_t e = launch_cover(cover_of<V>(a.dim), g.pieces + zero_units, [&](const Cover& c, dim3 blocks) {
         run_sum_kernel<EG, EO, V><<<blocks, kThreads, 0, s>>>(in, g, c);
