@@ -21,7 +21,7 @@
 // Measured on MI355X. Lookup of 16384 rows of 151936 x 2048 bfloat16 into float32: 33
 // us for 164 MB (5.0 TB/s; one row per thread instead of four: 49). Gradient of 16384
 // positions x 4096 bfloat16 into a bfloat16 table of 32000: 100 us in all, of which
-// the sort takes 17, the sum and the zeros 74 (396 MB at 5.3 TB/s) and the join 9; of
+// the sort takes 16, the sum and the zeros 60 to 74 (396 MB) and the join 8; of
 // 65536 positions x 256 into float32 x 151936: 69 us (sort 25, sum 27, join 8); of 100
 // positions: 12 us in three launches. Large sums are bound by memory, small ones by
 // the launches, which depend on one another.

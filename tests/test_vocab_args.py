@@ -143,7 +143,8 @@ def test_good_calls_without_a_device():
 def test_workspace_sizes_at_the_limits(items, beams, vocab, n_select):
     for code in (qqe.KLD_DTYPE_F32, qqe.KLD_DTYPE_BF16):
         n = qqe.kld_eval_beam_select_workspace(vocab, code, items, beams, n_select)
-        assert 0 < n < 2**46
+        rows = items * beams   # a sixteenth of the largest logits, a tile and a slice per row, a full chip's slices
+        assert 0 < n <= rows * (vocab // 4 + 256) + 16 * 8192 and n < 2**62
     assert 0 < qqe.kld_eval_embed_grad_workspace(vocab, 2**24, items) < 2**52
 
 
