@@ -198,10 +198,9 @@ GradSpace grad_space(void* ws, int64_t vocab, int64_t dim, int64_t n_tokens, int
     g.piece = kMostPiece;
     while (g.piece > kLeastPiece && n_tokens / g.piece * ((dim + 255) / 256) < kPieceWaves) g.piece /= 2;
     g.pieces = static_cast<int>((n_tokens + g.piece - 1) / g.piece);
-    char* p = static_cast<char*>(ws);
     int64_t at = 0;
-    const auto take = [&](int64_t n) {
-        char* q = p + at;
+    const auto take = [&](int64_t n) {  // ws is null where only the size is asked for
+        char* q = ws ? static_cast<char*>(ws) + at : nullptr;
         at += align16(n * 4);
         return q;
     };
