@@ -547,7 +547,8 @@ kld_status kld_eval_embed(const void* table, int32_t table_dtype, int64_t vocab,
  * once to out_dtype. Ids outside [0, vocab) add nothing.
  *   grad         device [n_tokens, dim] rows of grad_dtype, grad_stride
  *                elements apart (>= dim); n_tokens at most 4,194,304
- *   out          [vocab, dim] rows of out_dtype, out_stride elements apart
+ *   out          [vocab, dim] rows of out_dtype, out_stride elements apart;
+ *                vocab at most 2^24
  *   accumulate   0: every row is written, zero where no token names it;
  *                otherwise the sums are added to what `out` holds (rows that
  *                no token names are left as they are)

@@ -800,7 +800,7 @@ def beam_select(logits, scores, k=None, finished=None, eos_token: int = -1, out=
     ws = _workspace(workspace, nbytes, device, stream)
     _call(device, load_library().kld_eval_beam_select, logits.data_ptr(), code, vocab, stride, items, beams, k,
           _per(scores, per_beam, f32, "scores", device),
-          0 if finished is None else _per(finished, per_beam, u8, "finished", device), eos_token,
+          0 if finished is None else _per(finished, per_beam, u8, "finished", device), int(eos_token),
           _per(s, shape, f32, "out[0]", device), _per(p, shape, i32, "out[1]", device),
           _per(t, shape, i32, "out[2]", device), _per(f, shape, u8, "out[3]", device), ws.data_ptr(), ws.numel(),
           _raw_stream(stream, device))
@@ -846,7 +846,7 @@ def beam_reorder(states, parents, lengths=None, length_dim=None, stream=None) ->
     -1 leaves the row as it is).
 
     ``states``: a tensor or a sequence of tensors [items * beams, ...] of any
-    type (caches, token histories); ``parents`` int32 [items, beams], as
+    type (caches, token histories), none sharing memory with another; ``parents`` int32 [items, beams], as
     ``beam_select`` returns it with k = beams. With ``length_dim`` and
     ``lengths`` (int32 [items]) only that dimension's first positions of each
     item move, the rest stays as it is; the dimensions behind length_dim are
@@ -914,8 +914,8 @@ def embed(table, tokens, scale: float = 1.0, out=None, dtype=None, stream=None):
         if tuple(out.shape) != (*tokens.shape, dim):
             raise ValueError(f"out: expected shape {(*tokens.shape, dim)}, got {tuple(out.shape)}")
         o, ostride = out.data_ptr(), _rows_of(_as_rows(out, n, dim, "out"), "out", device)
-    _call(device, load_library().kld_eval_embed, table.data_ptr(), code, vocab, dim, stride, tk, n, scale, o, ocode,
-          ostride, _raw_stream(stream, device))
+    _call(device, load_library().kld_eval_embed, table.data_ptr(), code, vocab, dim, stride, tk, n, float(scale), o,
+          ocode, ostride, _raw_stream(stream, device))
     return out
 
 
@@ -929,8 +929,8 @@ def embed_grad(grad, tokens, vocab: int, scale: float = 1.0, out=None, dtype="f3
     """Gradient of ``embed`` with respect to its table: row v of the result is
     scale * the sum of grad[n] over the positions n with tokens[n] == v (ids
     outside [0, vocab) add nothing). ``grad`` is tokens.shape + (dim,),
-    bfloat16 or float32; returns [vocab, dim] of ``dtype`` (or ``out``, of its
-    own type), every row written. With ``accumulate`` the sums are added to
+    bfloat16 or float32; vocab at most 2^24; returns [vocab, dim] of ``dtype``
+    (or ``out``, of its own type), every row written. With ``accumulate`` the sums are added to
     ``out``."""
     device = _device_of(grad, "grad")
     if grad.dim() < 1 or tuple(grad.shape[:-1]) != tuple(tokens.shape):
@@ -948,8 +948,8 @@ def embed_grad(grad, tokens, vocab: int, scale: float = 1.0, out=None, dtype="f3
         raise ValueError(f"out: expected shape {(vocab, dim)}, got {tuple(out.shape)}")
     ostride = _rows_of(out, "out", device)
     ws = _workspace(workspace, nbytes, device, stream)
-    _call(device, load_library().kld_eval_embed_grad, rows.data_ptr(), gcode, gstride, tk, n, vocab, dim, scale,
-          out.data_ptr(), _dtype_code(out.dtype), ostride, 1 if accumulate else 0, ws.data_ptr(), ws.numel(),
+    _call(device, load_library().kld_eval_embed_grad, rows.data_ptr(), gcode, gstride, tk, n, vocab, dim,
+          float(scale), out.data_ptr(), _dtype_code(out.dtype), ostride, 1 if accumulate else 0, ws.data_ptr(), ws.numel(),
           _raw_stream(stream, device))
     return out
 

@@ -493,6 +493,15 @@ kld_status check_table(const char* who, int64_t vocab, int64_t dim, int64_t n_to
     return KLD_OK;
 }
 
+// The gradient's sort reads every id once per 512 rows of a table of more than 2^20.
+kld_status check_grad_sizes(const char* who, int64_t vocab, int64_t dim, int64_t n_tokens) {
+    const kld_status st = check_table(who, vocab, dim, n_tokens);
+    if (st != KLD_OK) return st;
+    if (vocab > (int64_t{1} << 24)) return fail(KLD_ERR_RANGE, std::string(who) + ": vocab exceeds 2^24");
+    if (n_tokens > kMaxVocabRows) return fail(KLD_ERR_RANGE, std::string(who) + ": n_tokens exceeds 4194304");
+    return KLD_OK;
+}
+
 kld_status check_rows(const char* who, const char* what, const void* p, int32_t dtype, int64_t n, int64_t dim,
                       int64_t stride) {
     if (!p) return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": " + what + " is NULL");
@@ -1112,9 +1121,8 @@ kld_status kld_eval_embed_grad_workspace(int64_t vocab, int64_t dim, int64_t n_t
     const char* who = "kld_eval_embed_grad_workspace";
     if (!bytes_out) return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": bytes_out is NULL");
     *bytes_out = 0;
-    const kld_status st = check_table(who, vocab, dim, n_tokens);
+    const kld_status st = check_grad_sizes(who, vocab, dim, n_tokens);
     if (st != KLD_OK) return st;
-    if (n_tokens > kMaxVocabRows) return fail(KLD_ERR_RANGE, std::string(who) + ": n_tokens exceeds 4194304");
     *bytes_out = kldk::embed_grad_workspace_bytes(vocab, dim, n_tokens);
     return KLD_OK;
 }
@@ -1127,9 +1135,8 @@ kld_status kld_eval_embed_grad(const void* grad, int32_t grad_dtype, int64_t gra
     const char* who = "kld_eval_embed_grad";
     if (!is_dtype(grad_dtype) || !is_dtype(out_dtype))
         return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": dtype must be KLD_DTYPE_F32 or KLD_DTYPE_BF16");
-    kld_status st = check_table(who, vocab, dim, n_tokens);
+    kld_status st = check_grad_sizes(who, vocab, dim, n_tokens);
     if (st != KLD_OK) return st;
-    if (n_tokens > kMaxVocabRows) return fail(KLD_ERR_RANGE, std::string(who) + ": n_tokens exceeds 4194304");
     if (!std::isfinite(scale)) return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": scale is not finite");
     if (n_tokens == 0 && accumulate) return KLD_OK;
     st = check_rows(who, "out", out, out_dtype, vocab, dim, out_stride);

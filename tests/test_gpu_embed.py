@@ -135,7 +135,9 @@ def test_gradient(vocab, dim, n, kind, ti, to):
 @pytest.mark.parametrize("ti,to", [("bf16", "bf16"), ("f32", "f32")])
 @pytest.mark.parametrize("n,vocab,dim,kind", [(70000, 1000, 24, "one"), (70000, 40000, 24, "words"),
                                               (200000, 3, 9, "uniform"), (131072, 151936, 8, "words"),
-                                              (40000, 300, 520, "words")])
+                                              (40000, 300, 520, "words"), (1537, 1 << 20, 4, "words"),
+                                              (20000, (1 << 20) + 1, 4, "words"), (1536, 5, 100, "few"),
+                                              (3000, 1 << 24, 1, "uniform")])
 def test_gradient_of_long_runs(n, vocab, dim, kind, ti, to):
     """Runs of thousands of positions, against sums in float64."""
     grad, tok = rand((n, dim), ti, 3), ids(n, vocab, 4, kind)

@@ -122,7 +122,7 @@ def test_embed_grad_refuses(kw):
 def test_embed_limits_and_empty():
     assert embed(n=0, table=None, tokens=None, out=None) == OK
     assert embed_grad(n=0, acc=1, grad=None, tokens=None, out=None, ws=None) == OK
-    assert embed_grad(n=2**22 + 1) == RANGE
+    assert embed_grad(n=2**22 + 1) == RANGE and embed_grad(vocab=2**24 + 1) == RANGE
     with pytest.raises(qqe.KldEvalError) as e:
         qqe.kld_eval_embed_grad_workspace(100, 8, 2**22 + 1)
     assert e.value.status == RANGE
@@ -145,7 +145,7 @@ def test_workspace_sizes_at_the_limits(items, beams, vocab, n_select):
         n = qqe.kld_eval_beam_select_workspace(vocab, code, items, beams, n_select)
         rows = items * beams   # a sixteenth of the largest logits, a tile and a slice per row, a full chip's slices
         assert 0 < n <= rows * (vocab // 4 + 256) + 16 * 8192 and n < 2**62
-    assert 0 < qqe.kld_eval_embed_grad_workspace(vocab, 2**24, items) < 2**52
+    assert 0 < qqe.kld_eval_embed_grad_workspace(min(vocab, 2**24), 2**24, items) < 2**52
 
 
 # ---- the torch-facing functions: host tensors and wrong shapes are refused ----
