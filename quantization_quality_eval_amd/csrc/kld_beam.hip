@@ -17,10 +17,10 @@
 // workgroup reads the rows concerned again in float64 and ranks once more.
 //
 // Measured on MI355X (kernel times). 128 items x 8 beams of 151936 bfloat16, one
-// beam in eight finished, K = 16: scan 51 us, 272 MB at 5.3 TB/s, of which about 22
+// beam in eight finished, K = 16: scan 50 us, 272 MB at 5.4 TB/s, of which about 30
 // us are vector instructions; merge 14 us. 32 x 4, K = 8: 9.5 + 11 us. 4 rows of
 // 32000: 3.9 + 8.7 us. Candidate lists kept by the scan's waves cost 62 to 72 us for
-// the largest case instead of 51: a list has a handful of arrivals per tile for
+// the largest case instead of 50: a list has a handful of arrivals per tile for
 // most of a row, and each cost more instructions than the tile's exponentials.
 #include <float.h>
 #include <hip/hip_runtime.h>
@@ -108,14 +108,17 @@ struct Row {
     __device__ __forceinline__ int loose_id(int i) const { return i < head ? i : tail_at + (i - head); }
 };
 
+// Signed order of float values (none is NaN), its own inverse on the bits.
+__device__ __forceinline__ int signed_order(int bits) { return bits ^ ((bits >> 31) & 0x7fffffff); }
 // Maximum over the 16 lanes of a row: with the neighbour, the other pair of the
-// quad, the other quad of the half, the other half.
+// quad, the other quad of the half, the other half. On integers it is one
+// instruction a step; on floats the compiler quiets both operands first.
 template <int kCtrl>
-__device__ __forceinline__ float max_with(float x) {
-    return fmaxf(x, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), kCtrl, 0xf, 0xf, true)));
+__device__ __forceinline__ int max_with(int x) {
+    return max(x, __builtin_amdgcn_mov_dpp(x, kCtrl, 0xf, 0xf, true));
 }
-__device__ __forceinline__ float row_max(float x) {
-    return max_with<0x140>(max_with<0x141>(max_with<0x4e>(max_with<0xb1>(x))));
+__device__ __forceinline__ int row_max(float x) {
+    return max_with<0x140>(max_with<0x141>(max_with<0x4e>(max_with<0xb1>(signed_order(__float_as_int(x))))));
 }
 
 // One wave per slice of a row, a tile of 2048 (1024) elements at a time with the
@@ -191,14 +194,14 @@ __global__ void __launch_bounds__(kWaves * 64)
         }
         sum = sum * static_cast<double>(__builtin_amdgcn_exp2f(ref - to)) + static_cast<double>(part);
         ref = to;
-        float mine = row_max(best[0]);
+        int mine = row_max(best[0]);
 #pragma unroll
         for (int u = 1; u < kChunks; ++u) {
-            const float q = row_max(best[u]);
+            const int q = row_max(best[u]);
             mine = (lane & 3) == u ? q : mine;
         }
         static_assert(kChunks == 4 && kGroupChunks == 16, "");
-        if ((lane & 12) == 0) *top = mine;
+        if ((lane & 12) == 0) *top = __int_as_float(signed_order(mine));
         top += kTileGroups;
     }
     if (slice == 0 && lane < in.loose) {
