@@ -225,6 +225,48 @@ def test_outputs_in_place_and_untouched_neighbours(dtype):
         qqe.beam_select(z, scores, workspace=ws[:nbytes - 1])
 
 
+@pytest.mark.parametrize("junk", [0.0, float("inf"), float("-inf"), float("nan"), 3e38])
+def test_whatever_the_workspace_holds(junk):
+    """Finished and empty beams leave their part of the workspace unwritten:
+    what it held before does not show."""
+    z, scores, _ = make(5, 4, 6000, "bf16", seed=14)
+    fin = torch.zeros(5, 4, dtype=torch.uint8, device=DEV)
+    fin[0, 1], fin[1], fin[2, 0] = 1, 1, 1
+    scores[2, 3], scores[3], scores[4, :3] = float("-inf"), float("-inf"), float("nan")
+    nbytes = qqe.beam_workspace_bytes(6000, 5, 4, 4, "bf16")
+    ws = torch.full(((nbytes + 3) // 4,), junk, device=DEV).view(torch.uint8)
+    run_and_check(z, scores, 4, fin, 9, ctx=f"workspace of {junk}", workspace=ws)
+
+
+def test_threads_on_streams_of_their_own():
+    """Four threads at once, each on its own stream, some with equal beams (rows
+    taken again in float64): each gets what it gets alone."""
+    import threading
+    cases = []
+    for i in range(4):
+        z, scores, _ = make(3 + i, 3, 5000 + 7 * i, ("f32", "bf16")[i % 2], seed=30 + i)
+        if i > 1:
+            z[1], scores[0, 1] = z[0], scores[0, 0]
+        cases.append((z, scores, qqe.beam_select(z, scores, 6)))
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(z, scores, want):
+        stream = torch.cuda.Stream()
+        for _ in range(25):
+            got = qqe.beam_select(z, scores, 6, stream=stream)
+            stream.synchronize()
+            if not all(torch.equal(a.cpu(), b.cpu()) for a, b in zip(got, want)):
+                bad.append(tuple(z.shape))
+
+    threads = [threading.Thread(target=work, args=c) for c in cases]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not bad
+
+
 def test_same_bits_every_time_and_on_another_stream():
     z, scores, _ = make(16, 4, 151936, "bf16", seed=10)
     first = qqe.beam_select(z, scores, 8)

@@ -169,6 +169,18 @@ def test_gradient_strides_and_untouched_bytes():
     assert torch.equal(three, qqe.embed_grad(wide[:, :60], tok, vocab))
 
 
+@pytest.mark.parametrize("fill", [0, 255, 127])
+@pytest.mark.parametrize("n", [70, 5000])
+def test_gradient_whatever_the_workspace_holds(n, fill):
+    vocab, dim = 400, 36
+    grad, tok = rand((n, dim), "f32", n), ids(n, vocab, n, "words")
+    ws = torch.full((qqe.embed_grad_workspace_bytes(vocab, dim, n),), fill, dtype=torch.uint8, device=DEV)
+    got = f64(qqe.embed_grad(grad, tok, vocab, workspace=ws))
+    want, mag, count = ov.embed_grad(synth.to_numpy_bits(grad), tok.cpu().numpy(), vocab)
+    close(got, want, half_step("f32") * np.abs(want) + 2.0 ** -24 * np.maximum(count - 1, 0)[:, None] * mag * 1.001,
+          f"workspace of {fill}")
+
+
 def test_gradient_of_no_tokens_and_bad_rows():
     out = rand((50, 33), "f32", 1)
     keep = out.clone()
