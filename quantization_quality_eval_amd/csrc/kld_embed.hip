@@ -600,11 +600,13 @@ __global__ void __launch_bounds__(kThreads) run_join_kernel(GradIn<EG, EO> a, Gr
     const int64_t block = c.first + blockIdx.x;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t piece = block / c.tiles, col = (block % c.tiles * 64 + lane) * V;
-    const int64_t total = *g.total, i0 = piece * g.piece, i1 = i0 + g.piece;
-    if (i1 >= total) return;
-    const int32_t word = g.word[i1 - 1];
-    if (g.word[i1] != word) return;                                      // no run leaves this piece
-    if (g.word[i0] == word && i0 > 0 && g.word[i0 - 1] == word) return;  // it began before
+    const int64_t i0 = piece * g.piece, i1 = i0 + g.piece;  // below n_tokens: the last piece has no unit
+    // read together, judged after: most units end here (6.9 us to 6.6 for 8192 tokens
+    // of 1000 columns); past the total the words hold anything and decide nothing
+    const int64_t total = *g.total;
+    const int32_t word = g.word[i1 - 1], behind = g.word[i1], first = g.word[i0], ahead = i0 > 0 ? g.word[i0 - 1] : -1;
+    if (i1 >= total || behind != word) return;   // no run leaves this piece
+    if (first == word && ahead == word) return;  // it began before
     const bool in_run = lane < g.piece && g.word[i0 + lane] == word;  // the piece's last positions
     const int64_t begin = i1 - __popcll(__ballot(in_run));
     const int64_t mask = (int64_t{1} << g.lg) - 1;
