@@ -235,6 +235,15 @@ __device__ __forceinline__ int wave_prefix(int c, int lane, int* sum) {
     return incl - c;
 }
 
+// Between LDS writes of a wave's lanes and reads of them by its other lanes. The
+// hardware runs a wave's LDS operations in order; the fences, which cost no
+// instruction, keep the compiler to that order as well.
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // The wave's lanes of `valid` that hold the same key (of `bits` bits) as this one.
 __device__ __forceinline__ unsigned long long same_key(unsigned long long valid, int key, int bits) {
     unsigned long long m = valid;
@@ -267,14 +276,14 @@ __global__ void __launch_bounds__(kThreads)
         }
     };
     for (int j = lane; j < g.owned; j += 64) own[j] = 0;
-    __builtin_amdgcn_wave_barrier();
+    wave_sync();
     int less = 0;
     each([&](int64_t, int32_t t) {
         const bool ok = t >= 0 && t < vocab;
         less += __popcll(__ballot(ok && (t & mask) < p));
         if (ok && (t & mask) == p) atomicAdd(&own[t >> g.lg], 1);
     });
-    __builtin_amdgcn_wave_barrier();
+    wave_sync();
     int sum = less;  // exclusive prefix over the owned ids, after the ids of the waves before
     for (int j0 = 0; j0 < g.owned; j0 += 64) {
         const int j = j0 + lane;
@@ -287,7 +296,7 @@ __global__ void __launch_bounds__(kThreads)
         }
         sum += all;
     }
-    __builtin_amdgcn_wave_barrier();
+    wave_sync();
     if (p == mask && lane == 0) {
         *g.total = sum;
         g.word[sum] = -1;
@@ -299,14 +308,14 @@ __global__ void __launch_bounds__(kThreads)
             const int x = __shfl(id, __builtin_ctzll(m));
             const unsigned long long same = __ballot(id == x) & m;
             const int at = own[x];
-            __builtin_amdgcn_wave_barrier();
+            wave_sync();
             if ((same >> lane) & 1) {
                 const int to = at + __popcll(same & below);
                 g.perm[to] = static_cast<int32_t>(n);
                 g.word[to] = t;
             }
             if (lane == 0) own[x] = at + __popcll(same);
-            __builtin_amdgcn_wave_barrier();
+            wave_sync();
             m &= ~same;
         }
     });
@@ -382,14 +391,14 @@ __global__ void __launch_bounds__(kSortThreads)
         const int key = x & (kBuckets - 1);
         const unsigned long long same = same_key(__ballot(ok), key, kLgBuckets);
         const int first = ok ? place[wave][key] : 0;
-        __builtin_amdgcn_wave_barrier();
+        wave_sync();
         if (ok) {
             const int to = first + __popcll(same & ((1ull << lane) - 1));
             g.bperm[to] = static_cast<int32_t>(n);
             g.bword[to] = x;
             if (same >> lane == 1) place[wave][key] = to + 1;  // the last of its residue
         }
-        __builtin_amdgcn_wave_barrier();
+        wave_sync();
     }
 }
 
@@ -447,14 +456,14 @@ __global__ void __launch_bounds__(kThreads) bucket_group_kernel(GradSpace g, int
             const int key = x[q] >> kLgBuckets;
             const unsigned long long same = same_key(__ballot(ok), key, id_bits);
             const int first = ok ? place[wave][key] : 0;
-            __builtin_amdgcn_wave_barrier();
+            wave_sync();
             if (ok) {
                 const int to = first + __popcll(same & ((1ull << lane) - 1));
                 g.perm[to] = n_of[q];
                 g.word[to] = x[q];
                 if (same >> lane == 1) place[wave][key] = to + 1;
             }
-            __builtin_amdgcn_wave_barrier();
+            wave_sync();
         }
     }
 }
