@@ -13,8 +13,9 @@
 // reach the bound again -- every chosen candidate is in one of them, as K of them
 // hold a candidate that good -- and ranks their elements in float64. The
 // normalisers come from float32 exponentials; where two neighbours of the
-// ranking, of different beams, are closer than those can tell, the item's
-// workgroup reads the rows concerned again in float64 and ranks once more.
+// ranking, of different beams, are closer than those can tell, or the last chosen
+// and any candidate of another beam behind it, the item's workgroup reads the rows
+// concerned again in float64 and ranks once more.
 //
 // Measured on MI355X (kernel times). 128 items x 8 beams of 151936 bfloat16, one
 // beam in eight finished, K = 16: scan 50 us, 272 MB at 5.4 TB/s, of which about 30
@@ -281,7 +282,7 @@ struct Merge {
     double list_s[kMergeList];   // candidates: score,
     uint64_t list_k[kMergeList]; // beam and logit, the first of equal scores with the least,
     int list_v[kMergeList];      // id
-    Scored ranked[kBeamMaxSelect + 1];
+    Scored ranked[kBeamMaxSelect];
     Scored pick[kMergeThreads / 64];
     double part[kMergeThreads / 64];
     float bound[kMergeThreads / 64][2];
@@ -299,6 +300,18 @@ struct Merge {
         list_s[at] = c.s;
         list_k[at] = (static_cast<uint64_t>(c.w) << 32) | ~order_of(c.z);
         list_v[at] = c.v;
+    }
+    // The beam's normaliser is too coarse for the order: it is taken again.
+    __device__ __forceinline__ void ask(int w) {
+        if (state[w] == kLive) state[w] = kRetake, again = 1;
+    }
+    // Whether a candidate that was not chosen may belong before the last chosen one. It
+    // need not be the next in order: others of the last one's beam, equal logits for
+    // instance, can stand between.
+    __device__ __forceinline__ void ask_near(const Scored& last, double s, int w, double tol) {
+        if (w == last.w || last.s - s > tol || s > last.s || (s == last.s && w < last.w)) return;
+        ask(w);
+        ask(last.w);
     }
     // The list's first m entries in order; four lanes per entry count the ones
     // before it, without a branch: equal logits of one beam are common.
@@ -402,32 +415,37 @@ __device__ __attribute__((noinline)) void retake(Merge& s, const Item<E>& item) 
 
 // Too many candidates near one another (long ties): the first m <= most one
 // after the other. A group is looked into where its largest logit beats what
-// the thread has found. Returns m.
+// the thread has found. One more pass asks for the beams with candidates near the
+// last one. Returns m.
 template <class E>
-__device__ __attribute__((noinline)) int pick_slowly(Merge& s, const Item<E>& item, int most) {
+__device__ __attribute__((noinline)) int pick_slowly(Merge& s, const Item<E>& item, int most, double tol) {
     constexpr int kW = kMergeThreads / 64, kPer = Elem<E>::kPer, kOfGroup = kGroupChunks * kPer;
     const Scored none{-INFINITY, -INFINITY, 0x7fffffff, 0x7fffffff};
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-    for (int j = 0; j < most; ++j) {
-        Scored best = none;
-        const auto consider = [&](const Scored& c) {
-            if ((j == 0 || before(s.ranked[j - 1], c)) && before(c, best)) best = c;
-        };
+    // f(candidate) for every candidate of the groups whose largest logit passes at(z, w)
+    const auto each = [&](auto&& at, auto&& f) {
         for (int w = 0; w < item.n_beams; ++w) {
             if (!s.live(w)) continue;
             const Row<E> row = item.row(w);
             for (int i = t; i < item.groups; i += kMergeThreads) {
                 const float z = item.tops[static_cast<int64_t>(w) * item.groups + i];
-                if (!(z > -INFINITY) || !(s.scored(z, w, 0).s > best.s || (best.w == w && z > best.z))) continue;
+                if (!(z > -INFINITY) || !at(z, w)) continue;
                 for (int e = 0; e < kOfGroup; ++e) {
                     const int64_t v = row.head + int64_t{i} * kOfGroup + e;
                     if (v >= row.tail_at) break;
                     const float x = widen(row.p[v]);
-                    if (isfinite(x)) consider(s.scored(x, w, static_cast<int>(v)));
+                    if (isfinite(x)) f(s.scored(x, w, static_cast<int>(v)));
                 }
             }
         }
-        item.each_loose(s, consider);
+        item.each_loose(s, f);
+    };
+    for (int j = 0; j < most; ++j) {
+        Scored best = none;
+        const auto consider = [&](const Scored& c) {
+            if ((j == 0 || before(s.ranked[j - 1], c)) && before(c, best)) best = c;
+        };
+        each([&](float z, int w) { return s.scored(z, w, 0).s > best.s || (best.w == w && z > best.z); }, consider);
         for (int d = 32; d >= 1; d >>= 1) {
             const Scored other{__shfl_xor(best.s, d), __shfl_xor(best.z, d), __shfl_xor(best.w, d),
                                __shfl_xor(best.v, d)};
@@ -442,6 +460,9 @@ __device__ __attribute__((noinline)) int pick_slowly(Merge& s, const Item<E>& it
         if (t == 0) s.ranked[j] = best;
         __syncthreads();
     }
+    const Scored last = s.ranked[most - 1];
+    each([&](float z, int w) { return w != last.w && last.s - s.scored(z, w, 0).s <= tol; },
+         [&](const Scored& c) { s.ask_near(last, c.s, c.w, tol); });
     return most;
 }
 
@@ -621,16 +642,23 @@ __global__ void __launch_bounds__(kMergeThreads)
             __syncthreads();
             const int n = s.count;
             fits = n <= kMergeList;
-            m = n < k + 1 ? n : k + 1;
+            m = n < k ? n : k;
             if (fits) s.rank(n, m);
             __syncthreads();
+            // the list holds whatever comes within tol of the last place
+            if (fits && m == k) {
+                const Scored last = s.ranked[k - 1];
+#pragma unroll 1
+                for (int i = t; i < n; i += kMergeThreads)
+                    s.ask_near(last, s.list_s[i], static_cast<int>(s.list_k[i] >> 32), tol);
+            }
         }
-        if (!fits) m = pick_slowly(s, item, k + 1);
+        if (!fits) m = pick_slowly(s, item, k, tol);
         if (t + 1 < m) {
             const Scored x = s.ranked[t], y = s.ranked[t + 1];
             if (x.w != y.w && x.s - y.s <= tol) {
-                if (s.state[x.w] == kLive) s.state[x.w] = kRetake, s.again = 1;
-                if (s.state[y.w] == kLive) s.state[y.w] = kRetake, s.again = 1;
+                s.ask(x.w);
+                s.ask(y.w);
             }
         }
         __syncthreads();
