@@ -46,17 +46,19 @@ constexpr int kHold = 6;             // quadruples of groups that a merge thread
 constexpr int kNear = 512;           // groups that the merge reads again at most
 
 constexpr float kLog2e = 1.44269504088896340736f;
-// Bounds of the float32 reference. Logits above the first, or rows that lie
-// below the second altogether, would lose their sums in float32: the merge
-// takes such rows in float64.
-constexpr float kMostRef = 1048576.0f * kLog2e;
-constexpr float kLeastRef = -32768.0f * kLog2e;
+// A sum's reference is its largest logit in binary units, rounded up to a whole
+// number: going over to a higher one multiplies the sum by a power of two, exactly,
+// however often a rising row does so. Bounds of the reference (logits of 2^20 and
+// -2^15). Logits above the first, or rows that lie below the second altogether, would
+// lose their sums in float32: the merge takes such rows in float64.
+constexpr float kMostRef = 1512776.0f;
+constexpr float kLeastRef = -47275.0f;
 
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-// Sum of a slice: sum 2^(z log2e - ref) over its finite logits. A NaN sum:
-// the slice holds logits past kMostRef.
+// Sum of a slice: sum 2^(z log2e - ref) over its finite logits, ref a whole number. A
+// NaN sum: the slice holds logits past kMostRef.
 struct Slice {
     double sum;
     float ref;
@@ -122,6 +124,13 @@ __device__ __forceinline__ int row_max(float x) {
     return max_with<0x140>(max_with<0x141>(max_with<0x4e>(max_with<0xb1>(signed_order(__float_as_int(x))))));
 }
 
+__device__ __forceinline__ float ref_of(float z) { return ceilf(z * kLog2e); }
+// A sum over the reference `from`, over `to` >= from. 2^-4096 of it is nothing: that
+// takes in references of infinity too.
+__device__ __forceinline__ double over(double sum, float from, float to) {
+    return ldexp(sum, static_cast<int>(fmaxf(from - to, -4096.0f)));
+}
+
 // One wave per slice of a row, a tile of 2048 (1024) elements at a time with the
 // next in flight; waves share nothing. Per lane a running reference and sum: the
 // exponentials of a tile are added in float32, tiles in float64. A tile costs
@@ -183,7 +192,7 @@ __global__ void __launch_bounds__(kWaves * 64)
 #pragma unroll
                 for (int e = 1; e < kPer; ++e) best[u] = fmaxf(best[u], x[u * kPer + e]);
             }
-            to = fmaxf(ref, fmaxf(fmaxf(best[0], best[1]), fmaxf(best[2], best[3])) * kLog2e);
+            to = fmaxf(ref, ref_of(fmaxf(fmaxf(best[0], best[1]), fmaxf(best[2], best[3]))));
             float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int i = 0; i < kEach; ++i) acc[i & 3] += __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], kLog2e, -to));
@@ -193,7 +202,7 @@ __global__ void __launch_bounds__(kWaves * 64)
 #pragma unroll
             for (int i = 0; i < kEach; ++i) x[i] = isfinite(x[i]) ? x[i] : -INFINITY;
         }
-        sum = sum * static_cast<double>(__builtin_amdgcn_exp2f(ref - to)) + static_cast<double>(part);
+        sum = over(sum, ref, to) + static_cast<double>(part);
         ref = to;
         int mine = row_max(best[0]);
 #pragma unroll
@@ -208,16 +217,15 @@ __global__ void __launch_bounds__(kWaves * 64)
     if (slice == 0 && lane < in.loose) {
         const float z = widen(in.p[in.loose_id(lane)]);
         if (isfinite(z)) {
-            const float to = fmaxf(ref, z * kLog2e);
-            sum = sum * static_cast<double>(__builtin_amdgcn_exp2f(ref - to)) +
-                  static_cast<double>(__builtin_amdgcn_exp2f(__builtin_fmaf(z, kLog2e, -to)));
+            const float to = fmaxf(ref, ref_of(z));
+            sum = over(sum, ref, to) + static_cast<double>(__builtin_amdgcn_exp2f(__builtin_fmaf(z, kLog2e, -to)));
             ref = to;
         }
     }
     float whole = ref;
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) whole = fmaxf(whole, __shfl_xor(whole, o));
-    sum *= static_cast<double>(__builtin_amdgcn_exp2f(ref - whole));
+    sum = over(sum, ref, whole);
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o);
     if (lane == 0) out.slice[row * slices + slice] = Slice{whole <= kMostRef ? sum : static_cast<double>(NAN), whole, 0};
@@ -517,19 +525,19 @@ __global__ void __launch_bounds__(kMergeThreads)
         for (int i = g + group; i < slices; i += group) {
             q = parts[i];
             const float to = fmaxf(ref, q.ref);
-            sum = sum * static_cast<double>(__builtin_amdgcn_exp2f(ref - to)) +
-                  q.sum * static_cast<double>(__builtin_amdgcn_exp2f(q.ref - to));
+            sum = over(sum, ref, to) + over(q.sum, q.ref, to);
             ref = to;
         }
         float to = ref;
 #pragma unroll 1
         for (int o = group >> 1; o >= 1; o >>= 1) to = fmaxf(to, __shfl_xor(to, o));
-        sum *= static_cast<double>(__builtin_amdgcn_exp2f(ref - to));
+        sum = over(sum, ref, to);
 #pragma unroll 1
         for (int o = group >> 1; o >= 1; o >>= 1) sum += __shfl_xor(sum, o);
         if (g == 0) {
-            // a sum below 1/2 never reached its reference: all of the row lies below kLeastRef, or is excluded
-            const bool sound = st == kLive && sum > 0.5;
+            // a row that reaches its reference holds a logit less than a unit below it, and its sum 1/2; one
+            // below 1/4: all of the row lies below kLeastRef, or is excluded
+            const bool sound = st == kLive && sum > 0.25;
             s.score[w] = score;
             s.state[w] = st == kLive && !sound ? kRetake : st;
             s.lse[w] = sound ? (static_cast<double>(to) + log2_of(sum)) / static_cast<double>(kLog2e) : 0.0;
@@ -711,9 +719,10 @@ hipError_t launch_typed(const BeamArgs& a, void* workspace, hipStream_t stream) 
     if (e != hipSuccess) return e;
     // Twice what a float32 normaliser may be off, in nats and units of 2^-24: the
     // exponentials' arguments, rounded by one unit of themselves, average at most
-    // log2 V (a distribution's mean -log2 p) times ln 2; an exponential is off by 2
-    // units, and so are the rescalings of lanes and slices; 8 and 2 additions by one
-    // each; the logarithm by 3; log2 e by a quarter of the entropy.
+    // log2 V + 2 (a distribution's mean -log2 p, and a sum of 1/4 at least) times ln 2;
+    // an exponential is off by 2 units; 8 and 2 additions by one each; the logarithm by
+    // 3 ln 2; log2 e by a quarter of the entropy, 0.16 log2 V: 16 + 0.86 log2 V. Tiles,
+    // lanes and slices are joined exactly, in float64 and by powers of two.
     const double tol = 2.0 * 0x1p-24 * (24.0 + log2(static_cast<double>(a.vocab)));
     // whether a row may have elements outside its chunks
     constexpr int kPer = Elem<E>::kPer;

@@ -1,5 +1,14 @@
 """The order of beam selection at the edge of what float32 normalisers can tell:
-near ties that continue behind the last place."""
+near ties that continue behind the last place, and rows that rise for many tiles.
+
+Tolerances. A score s + z - lse is formed in float64 and rounded once to
+float32: 2^-24 of itself. lse is off by at most 2^-24 (24 + log2 V), the bound
+that the selection's own order rests on: an exponential's argument is rounded
+once (2^-24 of itself; weighted by the probabilities the arguments average at
+most log2 V + 2 binary units, of ln 2 nats each), the exponential by one step
+(2), no value passes through more than 10 float32 additions (10), the logarithm
+by 3 binary units (2.1), log2 e by a quarter of the entropy (0.16 log2 V):
+16 + 0.86 log2 V in all. Rescalings are by powers of two and exact."""
 import numpy as np
 import pytest
 import torch
@@ -12,6 +21,7 @@ from tests.gpu_util import say
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
 TYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+UNIT = 2.0 ** -24
 
 
 def same_choice(got, want, ctx):
@@ -81,3 +91,65 @@ def test_finished_beams_next_to_equal_tops():
     s[:, 1] = (s[:, 0] + best[:, 0]).astype(np.float32)
     for k in (1, 2, 4, 5):
         choose_and_compare(z, torch.tensor(s, device=DEV), k, "finished beams", fin, 11)
+
+
+# ---- rows that rise for many tiles of one slice ----------------------------
+
+STEPS = [1e-5, 1e-4, 1e-3, 1e-2, 1e-1]
+ROWS = 8192   # from here on one wave reads a whole row
+
+
+def rising(vocab, step, seed):
+    """float32 logits that rise by `step` from one tile of 1024 to the next."""
+    g = np.random.default_rng(seed)
+    tile = np.arange(vocab) // 1024
+    return (step * (tile + 0.25 * g.random(vocab)) - 3.0).astype(np.float32)
+
+
+def many_rows(vocab, beams):
+    """Logits of 8192 rows of which only the ones that are filled are read: the others' beams are empty."""
+    z = torch.empty(ROWS, vocab, device=DEV)
+    return z, torch.full((ROWS // beams, beams), float("-inf"), device=DEV)
+
+
+@pytest.mark.parametrize("vocab", [65536, 262144, 1 << 20])
+def test_normaliser_of_rising_rows(vocab):
+    z, scores = many_rows(vocab, 1)
+    rows = [rising(vocab, st, i) for i, st in enumerate(STEPS)]
+    rows += [r[::-1].copy() for r in rows]
+    for i, r in enumerate(rows):
+        z[i] = torch.from_numpy(r).to(DEV)
+        scores[i] = 0.0
+    say(f"[beam order] rising rows of {vocab}")
+    s, p, t, _ = (x.cpu().numpy() for x in qqe.beam_select(z, scores, 2))
+    for i, r in enumerate(rows):
+        x = r.astype(np.float64)
+        lse = ov.log_normalisers(x[None])[0]
+        order = np.lexsort((np.arange(vocab), -x))[:2]
+        assert t[i].tolist() == order.tolist() and p[i].tolist() == [0, 0]
+        want = x[order] - lse
+        err = np.abs(s[i].astype(np.float64) - want)
+        tol = UNIT * (np.abs(want) + 24 + np.log2(vocab))
+        assert (err <= tol).all(), f"row {i}: off by {(err / UNIT).max():.0f} units, bound {(tol / UNIT).max():.0f}"
+
+
+def test_order_of_rising_beams():
+    """A rising row against the same logits falling, the scores a few steps apart
+    either way: the candidates stand in the order of the scores."""
+    vocab = 1 << 20
+    z, scores = many_rows(vocab, 2)
+    gaps = [-61, -13, 13, 61]   # odd: never a difference of two logits
+    items, want = 0, []
+    for i, st in enumerate(STEPS):
+        r = rising(vocab, st, i)
+        both = np.stack([r, r[::-1]])
+        for gap in gaps:
+            s = np.array([[-0.5, -0.5 + gap * UNIT]], np.float32)
+            z[2 * items:2 * items + 2] = torch.from_numpy(both).to(DEV)
+            scores[items] = torch.from_numpy(s[0]).to(DEV)
+            want.append(ov.beam_select(both, s, 2))
+            items += 1
+    say(f"[beam order] rising and falling beams of {vocab}")
+    got = qqe.beam_select(z, scores, 2)
+    assert (got[1][items:] == -1).all()
+    same_choice([x[:items] for x in got], [np.concatenate(x) for x in zip(*want)], "rising and falling beams")
