@@ -483,7 +483,8 @@ kld_status kld_eval_compare_noalloc(const void* base, const void* quant, int64_t
  *   finished     uint8[n_items][n_beams], nonzero for a finished beam, or NULL
  *                for none; needs an eos_token
  *   eos_token    id that ends a beam, in [0, vocab), or -1 for none
- *   scores_out   float32[n_items][n_select]
+ *   scores_out   float32[n_items][n_select]  (a score past float32's range
+ *                becomes an infinity and keeps its parent and token)
  *   parents_out  int32[n_items][n_select]  the chosen candidate's beam
  *   tokens_out   int32[n_items][n_select]  its token
  *   finished_out uint8[n_items][n_select]  1 if the beam was finished or the

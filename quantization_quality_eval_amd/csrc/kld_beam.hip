@@ -282,7 +282,8 @@ __device__ __forceinline__ double log2_of(double x) {
 struct Merge {
     float score[kBeamMaxBeams];
     double lse[kBeamMaxBeams];
-    float shift[kBeamMaxBeams];  // score - lse, rounded; -inf for a beam that offers no logits
+    float shift[kBeamMaxBeams];  // score - lse, rounded; NaN where that passes float32's range; -inf for a
+                                 // beam that offers no logits
     int state[kBeamMaxBeams];
     f32x4 quad[kNear];           // quadruples with groups worth reading,
     int2 quad_at[kNear];         // their beams and first groups
@@ -296,7 +297,8 @@ struct Merge {
     float bound[kMergeThreads / 64][2];
     int count, quad_count, near_count, again;
     __device__ __forceinline__ void set_shift(int w) {
-        shift[w] = live(w) ? static_cast<float>(score[w] - lse[w]) : -INFINITY;
+        const float x = static_cast<float>(score[w] - lse[w]);
+        shift[w] = !live(w) ? -INFINITY : fabsf(x) < INFINITY ? x : NAN;
     }
     __device__ __forceinline__ bool live(int w) const { return state[w] == kLive || state[w] == kExact; }
     __device__ __forceinline__ Scored scored(float z, int w, int v) const {
@@ -559,7 +561,9 @@ __global__ void __launch_bounds__(kMergeThreads)
     for (;;) {
         // What k groups reach: each of the waves holds `share` lanes that reach the least
         // of their bounds, or one wave holds k. z + shift is formed in float32 here; shift
-        // and sum are off by 2^-24 of themselves, which is taken off the bounds.
+        // and sum are off by 2^-24 of themselves, which is taken off the bounds. A sum that
+        // cannot be formed (NaN) or that passes float32's range claims nothing, and nothing
+        // is left out for it: whether a token is excluded is a matter of its logit alone.
         float mine = -INFINITY;
         const auto look = [&](const f32x4& q, int w) {
             const float shift = s.shift[w], sc = best_of(q) + shift;
@@ -588,8 +592,8 @@ __global__ void __launch_bounds__(kMergeThreads)
             return least_f - 0x1p-22f * (fabsf(least_f) + fabsf(shift)) - 2.0f * static_cast<float>(tol);
         };
         const auto reaches = [&](const f32x4& q, int w) {
-            const float shift = s.shift[w], sc = best_of(q) + shift;
-            return sc > -INFINITY && sc >= reach(shift);
+            const float shift = s.shift[w], best = best_of(q);
+            return shift != -INFINITY && best > -INFINITY && !(best + shift < reach(shift));
         };
         const auto take = [&](const f32x4& q, int i, int w) {
             if (!reaches(q, w)) return;
@@ -612,7 +616,7 @@ __global__ void __launch_bounds__(kMergeThreads)
             const float z = reinterpret_cast<const float*>(s.quad)[i];
             const int2 q = s.quad_at[i >> 2];
             const float shift = s.shift[q.x];
-            if (z > -INFINITY && z + shift >= reach(shift)) {
+            if (z > -INFINITY && !(z + shift < reach(shift))) {
                 const int at = atomicAdd(&s.near_count, 1);
                 if (at < kNear) s.near[at] = int2{q.x, q.y + (i & 3)};
             }
@@ -637,13 +641,13 @@ __global__ void __launch_bounds__(kMergeThreads)
 #pragma unroll
                     for (int e = 0; e < kPer / 4; ++e) {
                         const float z = Elem<E>::get(u32x4{word, 0, 0, 0}, e);
-                        if (z + shift >= from && isfinite(z)) s.add(s.scored(z, g.x, v + j * (kPer / 4) + e));
+                        if (isfinite(z) && !(z + shift < from)) s.add(s.scored(z, g.x, v + j * (kPer / 4) + e));
                     }
                 }
             }
             if (loose)
                 item.each_loose(s, [&](const Scored& c) {
-                    if (static_cast<float>(c.s) >= reach(s.shift[c.w])) s.add(c);
+                    if (!(static_cast<float>(c.s) < reach(s.shift[c.w]))) s.add(c);
                 });
             else if (t < n_beams && s.state[t] == kFinished)
                 s.add(Scored{static_cast<double>(s.score[t]), 0.0f, t, eos});

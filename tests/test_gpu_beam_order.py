@@ -1,5 +1,6 @@
 """The order of beam selection at the edge of what float32 normalisers can tell:
-near ties that continue behind the last place, and rows that rise for many tiles.
+near ties that continue behind the last place, rows that rise for many tiles,
+and logits whose range passes float32's.
 
 Tolerances. A score s + z - lse is formed in float64 and rounded once to
 float32: 2^-24 of itself. lse is off by at most 2^-24 (24 + log2 V), the bound
@@ -153,3 +154,53 @@ def test_order_of_rising_beams():
     got = qqe.beam_select(z, scores, 2)
     assert (got[1][items:] == -1).all()
     same_choice([x[:items] for x in got], [np.concatenate(x) for x in zip(*want)], "rising and falling beams")
+
+
+# ---- ranges past float32's ---------------------------------------------------
+
+def compare_far(z, scores, k, ctx):
+    """As above; a score past float32's range is rounded to -inf and keeps its parent and token."""
+    got, want = choose_and_compare(z, scores, k, ctx)
+    s, ws = got[0].cpu().numpy(), want[0]
+    with np.errstate(over="ignore"):
+        w32 = ws.astype(np.float32)
+    far = ~np.isfinite(w32)
+    assert np.array_equal(s[far], w32[far]), ctx
+    tol = UNIT * (np.abs(ws[~far]) + 24 + np.log2(z.shape[1]))
+    assert (np.abs(s[~far].astype(np.float64) - ws[~far]) <= tol).all(), ctx
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("vocab", [3000, 3001])
+def test_candidates_far_below_the_best(vocab, dtype):
+    """A token of the type's lowest value beside 1e38, so that its score lies past
+    float32's range: it is chosen when nothing else is left, wherever it stands."""
+    low, inf = torch.finfo(TYPES[dtype]).min, float("inf")
+    places = [0, 1, 40, 63, 64, 127, 1500, 2047, 2999]
+    z = torch.full((2 * len(places), vocab), -inf, device=DEV)
+    for i, at in enumerate(places):
+        z[2 * i, [200, 1400]] = 1e38
+        z[2 * i, at] = low
+        z[2 * i + 1, 2500] = 3.0e38
+        z[2 * i + 1, [at, (at + 700) % 2500]] = low
+    scores = torch.full((len(places), 2), -1.0, device=DEV)
+    scores[::2, 1] = -inf
+    for k in (2, 3, 4, 6, 8):
+        compare_far(z.to(TYPES[dtype]), scores, k, "far below the best")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_scores_and_normalisers_of_any_size(dtype):
+    """score - lse passes float32's range either way while the sums do not."""
+    vocab, sizes = 2050, [0.0, 1.0, 1e30, 3e38]
+    pairs = [(a * s, b * t) for a in sizes for b in sizes for s in (-1, 1) for t in (-1, 1)]
+    g = torch.Generator(device=DEV).manual_seed(8)
+    z = torch.randn(2 * len(pairs), vocab, generator=g, device=DEV)
+    scores = torch.zeros(len(pairs), 2, device=DEV)
+    for i, (score, base) in enumerate(pairs):
+        z[2 * i] += base
+        scores[i, 0] = score
+        scores[i, 1] = score if i % 2 else -5.0
+    z = z.to(TYPES[dtype])
+    for k in (1, 6, 64):
+        compare_far(z, scores, k, "any size")
