@@ -528,8 +528,8 @@ kld_status kld_eval_beam_reorder(void* const* states, int32_t n_states, int64_t 
                                  int64_t n_positions, int64_t position_bytes, const int32_t* lengths, void* stream);
 
 /*
- * Embedding lookup with scaling: out[n] = scale * table[tokens[n]], rounded
- * once to out_dtype (nearest even). A negative id gives a zero row, an id >=
+ * Embedding lookup with scaling: out[n] = scale * table[tokens[n]], formed in
+ * float64 and rounded once to out_dtype (nearest even). A negative id gives a zero row, an id >=
  * vocab a NaN row (it is never used as an address).
  *   table        device [vocab, dim] rows of table_dtype, table_stride elements
  *                apart (>= dim); dim 1 .. 2^24
@@ -544,8 +544,8 @@ kld_status kld_eval_embed(const void* table, int32_t table_dtype, int64_t vocab,
 /*
  * Gradient of the lookup with respect to the table:
  *   out[v] = scale * sum over { n : tokens[n] == v } of grad[n]
- * summed in float32 in an order that depends on the tokens alone, and rounded
- * once to out_dtype. Ids outside [0, vocab) add nothing.
+ * summed in float32 in an order fixed by the sizes and the tokens, scaled and
+ * added in float64, and rounded once to out_dtype. Ids outside [0, vocab) add nothing.
  *   grad         device [n_tokens, dim] rows of grad_dtype, grad_stride
  *                elements apart (>= dim); n_tokens at most 4,194,304
  *   out          [vocab, dim] rows of out_dtype, out_stride elements apart;

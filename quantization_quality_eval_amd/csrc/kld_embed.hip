@@ -42,20 +42,48 @@ constexpr int kOwned = 512;  // ids one wave owns at most
 __device__ __forceinline__ float widen(float x) { return x; }
 __device__ __forceinline__ float widen(uint16_t b) { return __uint_as_float(static_cast<unsigned int>(b) << 16); }
 
-// float -> bfloat16 bits, round to nearest even; NaN stays NaN.
+// float -> bfloat16 bits, round to nearest even; NaN stays NaN. One instruction for two.
 __device__ __forceinline__ uint16_t to_bf16(float x) {
-    const unsigned int u = __float_as_uint(x);
-    if ((u & 0x7fffffffu) > 0x7f800000u) return static_cast<uint16_t>((u >> 16) | 0x40u);
-    return static_cast<uint16_t>((u + 0x7fffu + ((u >> 16) & 1u)) >> 16);
+    return __builtin_bit_cast(uint16_t, static_cast<__bf16>(x));
 }
-__device__ __forceinline__ void put(float* p, float x) { *p = x; }
-__device__ __forceinline__ void put(uint16_t* p, float x) { *p = to_bf16(x); }
-
 // V consecutive elements as one load or store (V * sizeof(E) is 2 to 16 bytes).
 template <class E, int V>
 struct alignas(V * sizeof(E)) Vec {
     E x[V];
 };
+
+// V float64 results, each rounded once to nearest even. On its way to bfloat16 a
+// value is rounded to float32 first; as the midpoints of bfloat16 are float32 values,
+// that takes no value across one, but may put a value onto one that lies beside it.
+// Only there (one value in 65536) is the float64 looked at again: it says which side,
+// and a step of the float32 to that side rounds as it does.
+template <class EO, int V>
+__device__ __forceinline__ Vec<EO, V> rounded(const double (&x)[V]) {
+    Vec<EO, V> o;
+    if constexpr (sizeof(EO) == 4) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) o.x[e] = static_cast<float>(x[e]);
+    } else {
+        unsigned int u[V];
+        bool midpoint = false;
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            u[e] = __float_as_uint(static_cast<float>(x[e]));
+            midpoint |= (u[e] & 0xffffu) == 0x8000u;
+        }
+        if (midpoint) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                if ((u[e] & 0xffffu) != 0x8000u) continue;
+                const double here = fabs(static_cast<double>(__uint_as_float(u[e]))), from = fabs(x[e]);
+                u[e] += (here < from) - (here > from);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < V; ++e) o.x[e] = to_bf16(__uint_as_float(u[e]));
+    }
+    return o;
+}
 
 // How a launch covers rows and columns: `lanes` threads (a power of two from 64
 // to kThreads) of V elements each take one tile of a row's columns, tile after
@@ -131,16 +159,15 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int q = 0; q < R; ++q) {
         if (n0 + q >= n_tokens) break;
-        Vec<EO, V> o;
+        double z[V];
         if (t[q] >= 0 && t[q] < vocab) {
 #pragma unroll
-            for (int e = 0; e < V; ++e)
-                put(&o.x[e], static_cast<float>(static_cast<double>(widen(x[q].x[e])) * scale));
+            for (int e = 0; e < V; ++e) z[e] = static_cast<double>(widen(x[q].x[e])) * scale;
         } else {
 #pragma unroll
-            for (int e = 0; e < V; ++e) put(&o.x[e], t[q] < 0 ? 0.0f : NAN);
+            for (int e = 0; e < V; ++e) z[e] = t[q] < 0 ? 0.0 : static_cast<double>(NAN);
         }
-        *reinterpret_cast<Vec<EO, V>*>(out + (n0 + q) * out_stride + at.col) = o;
+        *reinterpret_cast<Vec<EO, V>*>(out + (n0 + q) * out_stride + at.col) = rounded<EO, V>(z);
     }
 }
 
@@ -524,13 +551,13 @@ __device__ __forceinline__ void finish(const GradIn<EG, EO>& a, int32_t word, in
     Vec<EO, V>* o = reinterpret_cast<Vec<EO, V>*>(a.out + word * a.out_stride + col);
     Vec<EO, V> v{};
     if (a.accumulate) v = *o;
+    double s[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-        double s = static_cast<double>(acc[e]) * a.scale;
-        if (a.accumulate) s += static_cast<double>(widen(v.x[e]));
-        put(&v.x[e], static_cast<float>(s));
+        s[e] = static_cast<double>(acc[e]) * a.scale;
+        if (a.accumulate) s[e] += static_cast<double>(widen(v.x[e]));
     }
-    *o = v;
+    *o = rounded<EO, V>(s);
 }
 
 template <class EG, class EO, int V>
