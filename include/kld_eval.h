@@ -522,7 +522,16 @@ kld_status kld_eval_beam_select(const void* logits, int32_t dtype, int64_t vocab
  *   lengths      int32[n_items], taken into [0, n_positions], or NULL for
  *                n_positions everywhere
  * A count of zero is a no-op.
+ *
+ * kld_eval_beam_reorder_check makes the call's checks of the states and their
+ * geometry alone, on the host, and enqueues nothing: states of several
+ * geometries take a call each, and a caller who has had all of them checked
+ * first is not left with some of them moved when a later one is refused.
  */
+kld_status kld_eval_beam_reorder_check(void* const* states, int32_t n_states, int64_t n_items, int32_t n_beams,
+                                       int64_t beam_stride, int64_t n_outer, int64_t outer_stride,
+                                       int64_t n_positions, int64_t position_bytes);
+
 kld_status kld_eval_beam_reorder(void* const* states, int32_t n_states, int64_t n_items, int32_t n_beams,
                                  const int32_t* parents, int64_t beam_stride, int64_t n_outer, int64_t outer_stride,
                                  int64_t n_positions, int64_t position_bytes, const int32_t* lengths, void* stream);

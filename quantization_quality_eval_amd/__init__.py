@@ -103,6 +103,7 @@ def load_library(build_if_missing: bool = True):
     f64, i64p = ctypes.c_double, ctypes.POINTER(i64)
     lib.kld_eval_beam_select_workspace.argtypes = [i64, i32, i64, i32, i32, i64p]
     lib.kld_eval_beam_select.argtypes = [vp, i32, i64, i64, i64, i32, i32, vp, vp, i32, vp, vp, vp, vp, vp, i64, vp]
+    lib.kld_eval_beam_reorder_check.argtypes = [ctypes.POINTER(vp), i32, i64, i32, i64, i64, i64, i64, i64]
     lib.kld_eval_beam_reorder.argtypes = [ctypes.POINTER(vp), i32, i64, i32, vp, i64, i64, i64, i64, i64, vp, vp]
     lib.kld_eval_embed.argtypes = [vp, i32, i64, i64, i64, vp, i64, f64, vp, i32, i64, vp]
     lib.kld_eval_embed_grad_workspace.argtypes = [i64, i64, i64, i64p]
@@ -114,7 +115,7 @@ def load_library(build_if_missing: bool = True):
               lib.kld_eval_copy_row_flags,
               lib.kld_eval_grad, lib.kld_eval_topk_compress, lib.kld_eval_rows_topk, lib.kld_eval_grad_topk,
               lib.kld_eval_read_probe, lib.kld_eval_compare_noalloc, lib.kld_eval_beam_select_workspace,
-              lib.kld_eval_beam_select, lib.kld_eval_beam_reorder, lib.kld_eval_embed,
+              lib.kld_eval_beam_select, lib.kld_eval_beam_reorder_check, lib.kld_eval_beam_reorder, lib.kld_eval_embed,
               lib.kld_eval_embed_grad_workspace, lib.kld_eval_embed_grad, lib.kld_eval_destroy):
         f.restype = ctypes.c_int
     lib.kld_eval_last_error.argtypes = []
@@ -288,6 +289,14 @@ def kld_eval_beam_select(logits: int, dtype: int, vocab: int, row_stride: int, n
         logits or None, dtype, vocab, row_stride, n_items, n_beams, n_select, scores or None, finished or None,
         eos_token, scores_out or None, parents_out or None, tokens_out or None, finished_out or None,
         workspace or None, workspace_bytes, stream or None))
+
+
+def kld_eval_beam_reorder_check(states, n_items: int, n_beams: int, beam_stride: int, n_outer: int, outer_stride: int,
+                                n_positions: int, position_bytes: int) -> int:
+    """states: device addresses, one per state."""
+    arr = (ctypes.c_void_p * len(states))(*states)
+    return _check(load_library().kld_eval_beam_reorder_check(arr, len(states), n_items, n_beams, beam_stride, n_outer,
+                                                             outer_stride, n_positions, position_bytes))
 
 
 def kld_eval_beam_reorder(states, n_items: int, n_beams: int, parents: int, beam_stride: int, n_outer: int,
@@ -846,8 +855,9 @@ def beam_reorder(states, parents, lengths=None, length_dim=None, stream=None) ->
     -1 leaves the row as it is).
 
     ``states``: a tensor or a sequence of tensors [items * beams, ...] of any
-    type (caches, token histories), none sharing memory with another; ``parents`` int32 [items, beams], as
-    ``beam_select`` returns it with k = beams. With ``length_dim`` and
+    type (caches, token histories), none sharing memory with another;
+    ``parents`` int32 [items, beams], as ``beam_select`` returns it with k =
+    beams. Where one state is refused none has been moved. With ``length_dim`` and
     ``lengths`` (int32 [items]) only that dimension's first positions of each
     item move, the rest stays as it is; the dimensions behind length_dim are
     contiguous, the ones between the first and it one stride apart."""
@@ -872,6 +882,9 @@ def beam_reorder(states, parents, lengths=None, length_dim=None, stream=None) ->
     pa = _per(parents, parents.shape, torch.int32, "parents", device)
     le = 0 if lengths is None else _per(lengths, torch.Size((items,)), torch.int32, "lengths", device)
     raw = _raw_stream(stream, device)
+    if len(groups) > 1:   # one call per geometry: all are checked before the first one moves anything
+        for (outer, step, positions, nbytes, beam), ptrs in groups.values():
+            kld_eval_beam_reorder_check(ptrs, items, beams, beam, outer, step, positions, nbytes)
     for (outer, step, positions, nbytes, beam), ptrs in groups.values():
         _call(device, load_library().kld_eval_beam_reorder, (ctypes.c_void_p * len(ptrs))(*ptrs), len(ptrs), items,
               beams, pa, beam, outer, step, positions, nbytes, le, raw)
@@ -959,7 +972,8 @@ __all__ = ["Evaluator", "Summary", "TokenSummary", "compare", "compare_tokens", 
            "kld_eval_reduce_segments", "kld_eval_copy_lse", "kld_eval_copy_row_flags", "kld_eval_grad", "kld_eval_topk_compress",
            "kld_eval_rows_topk", "kld_eval_grad_topk", "kld_eval_read_probe", "read_probe", "kld_eval_destroy",
            "kld_eval_compare_noalloc", "kld_eval_reduce_async", "summary_from_bytes",
-           "kld_eval_last_error", "kld_eval_beam_select_workspace", "kld_eval_beam_select", "kld_eval_beam_reorder",
+           "kld_eval_last_error", "kld_eval_beam_select_workspace", "kld_eval_beam_select",
+           "kld_eval_beam_reorder_check", "kld_eval_beam_reorder",
            "kld_eval_embed", "kld_eval_embed_grad_workspace", "kld_eval_embed_grad", "beam_workspace_bytes",
            "beam_select", "beam_reorder", "embed", "embed_grad_workspace_bytes", "embed_grad",
            "load_library", "build_library", "library_path", "KLD_DTYPE_F32", "KLD_DTYPE_BF16",

@@ -473,6 +473,42 @@ bool states_overlap(uint64_t d, int64_t rows, int64_t beam_stride, int64_t n_out
     return false;
 }
 
+// The checks of a reordering's states and geometry; *empty: there is nothing to move.
+kld_status check_states(const char* who, void* const* states, int32_t n_states, int64_t n_items, int32_t n_beams,
+                        int64_t beam_stride, int64_t n_outer, int64_t outer_stride, int64_t n_positions,
+                        int64_t position_bytes, bool* empty) {
+    *empty = false;
+    const kld_status st = check_beams(who, n_items, n_beams);
+    if (st != KLD_OK) return st;
+    if (n_states < 0 || n_outer < 0 || n_positions < 0 || position_bytes < 0)
+        return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": negative count");
+    *empty = n_states == 0 || n_items == 0 || n_outer == 0 || n_positions == 0 || position_bytes == 0;
+    if (*empty) return KLD_OK;
+    if (!states) return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": states is NULL");
+    for (int32_t k = 0; k < n_states; ++k)
+        if (!states[k]) return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": a state is NULL");
+    // [beam][outer][position] without overlap, in either order of the first two
+    const int64_t rows = n_items * n_beams;
+    if (product_over(n_positions, position_bytes, kMaxExtent) ||
+        (rows > 1 && product_over(rows - 1, beam_stride, kMaxExtent)) ||
+        (n_outer > 1 && product_over(n_outer - 1, outer_stride, kMaxExtent)))
+        return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": a state spans more than 2^56 bytes");
+    const int64_t inner = n_positions * position_bytes;
+    const bool beams_outside = (n_outer == 1 || outer_stride >= inner) &&
+                               (rows == 1 || beam_stride >= (n_outer - 1) * (n_outer == 1 ? 0 : outer_stride) + inner);
+    const bool beams_inside = (rows == 1 || beam_stride >= inner) &&
+                              (n_outer == 1 || outer_stride >= (rows - 1) * (rows == 1 ? 0 : beam_stride) + inner);
+    if (!beams_outside && !beams_inside)
+        return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": the strides make beams overlap");
+    for (int32_t k = 0; k < n_states; ++k)
+        for (int32_t j = 0; j < k; ++j) {
+            const uintptr_t x = reinterpret_cast<uintptr_t>(states[k]), y = reinterpret_cast<uintptr_t>(states[j]);
+            if (states_overlap(x > y ? x - y : y - x, rows, beam_stride, n_outer, outer_stride, inner))
+                return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": two states overlap");
+        }
+    return KLD_OK;
+}
+
 kld_status check_beam_shape(const char* who, int32_t dtype, int64_t vocab, int64_t n_items, int32_t n_beams,
                             int32_t n_select) {
     if (!is_dtype(dtype))
@@ -1048,40 +1084,27 @@ kld_status kld_eval_beam_select(const void* logits, int32_t dtype, int64_t vocab
     return KLD_OK;
 }
 
+kld_status kld_eval_beam_reorder_check(void* const* states, int32_t n_states, int64_t n_items, int32_t n_beams,
+                                       int64_t beam_stride, int64_t n_outer, int64_t outer_stride,
+                                       int64_t n_positions, int64_t position_bytes) {
+    const CallRange range_("kld_eval_beam_reorder_check");
+    bool empty;
+    return check_states("kld_eval_beam_reorder_check", states, n_states, n_items, n_beams, beam_stride, n_outer,
+                        outer_stride, n_positions, position_bytes, &empty);
+}
+
 kld_status kld_eval_beam_reorder(void* const* states, int32_t n_states, int64_t n_items, int32_t n_beams,
                                  const int32_t* parents, int64_t beam_stride, int64_t n_outer, int64_t outer_stride,
                                  int64_t n_positions, int64_t position_bytes, const int32_t* lengths, void* stream) {
     const CallRange range_("kld_eval_beam_reorder");
     const char* who = "kld_eval_beam_reorder";
-    kld_status st = check_beams(who, n_items, n_beams);
-    if (st != KLD_OK) return st;
-    if (n_states < 0 || n_outer < 0 || n_positions < 0 || position_bytes < 0)
-        return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": negative count");
-    if (n_states == 0 || n_items == 0 || n_outer == 0 || n_positions == 0 || position_bytes == 0) return KLD_OK;
-    if (!states || !parents) return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": states or parents is NULL");
-    for (int32_t k = 0; k < n_states; ++k)
-        if (!states[k]) return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": a state is NULL");
+    bool empty;
+    kld_status st = check_states(who, states, n_states, n_items, n_beams, beam_stride, n_outer, outer_stride,
+                                 n_positions, position_bytes, &empty);
+    if (st != KLD_OK || empty) return st;
+    if (!parents) return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": parents is NULL");
     if (!aligned(parents, 4) || !aligned(lengths, 4))
         return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": parents or lengths is not 4-byte aligned");
-    // [beam][outer][position] without overlap, in either order of the first two
-    const int64_t rows = n_items * n_beams;
-    if (product_over(n_positions, position_bytes, kMaxExtent) ||
-        (rows > 1 && product_over(rows - 1, beam_stride, kMaxExtent)) ||
-        (n_outer > 1 && product_over(n_outer - 1, outer_stride, kMaxExtent)))
-        return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": a state spans more than 2^56 bytes");
-    const int64_t inner = n_positions * position_bytes;
-    const bool beams_outside = (n_outer == 1 || outer_stride >= inner) &&
-                               (rows == 1 || beam_stride >= (n_outer - 1) * (n_outer == 1 ? 0 : outer_stride) + inner);
-    const bool beams_inside = (rows == 1 || beam_stride >= inner) &&
-                              (n_outer == 1 || outer_stride >= (rows - 1) * (rows == 1 ? 0 : beam_stride) + inner);
-    if (!beams_outside && !beams_inside)
-        return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": the strides make beams overlap");
-    for (int32_t k = 0; k < n_states; ++k)
-        for (int32_t j = 0; j < k; ++j) {
-            const uintptr_t x = reinterpret_cast<uintptr_t>(states[k]), y = reinterpret_cast<uintptr_t>(states[j]);
-            if (states_overlap(x > y ? x - y : y - x, rows, beam_stride, n_outer, outer_stride, inner))
-                return fail(KLD_ERR_INVALID_ARG, std::string(who) + ": two states overlap");
-        }
     st = current_device_ok(who);
     if (st != KLD_OK) return st;
     const kldk::ReorderArgs a{states,  n_states,     n_items,     n_beams,        parents, beam_stride,
