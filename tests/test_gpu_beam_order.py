@@ -1,6 +1,6 @@
 """The order of beam selection at the edge of what float32 normalisers can tell:
 near ties that continue behind the last place, rows that rise for many tiles,
-and logits whose range passes float32's.
+logits whose range passes float32's, and scores of long outputs.
 
 Tolerances. A score s + z - lse is formed in float64 and rounded once to
 float32: 2^-24 of itself. lse is off by at most 2^-24 (24 + log2 V), the bound
@@ -204,3 +204,42 @@ def test_scores_and_normalisers_of_any_size(dtype):
     z = z.to(TYPES[dtype])
     for k in (1, 6, 64):
         compare_far(z, scores, k, "any size")
+
+
+# ---- scores of long outputs --------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("score", [-60.0, -600.0, -1200.0, -5000.0, -40000.0])
+def test_scores_of_long_outputs(score, dtype):
+    """Beams that have generated hundreds of tokens."""
+    g = torch.Generator(device=DEV).manual_seed(13)
+    z = torch.randn(12, 50001, generator=g, device=DEV).mul_(3.0).to(TYPES[dtype])
+    scores = score - (torch.rand(3, 4, generator=g, device=DEV) * 6).sort(1).values
+    for k in (1, 4, 16):
+        compare_far(z, scores, k, f"scores of {score}")
+
+
+def test_scores_of_long_outputs_cost_no_more():
+    """The candidates that are ranked are the ones near the k-th best, however far
+    the scores lie from zero: a bound of 16 bits let nearly all groups pass at -600
+    and took 130 times as long."""
+    g = torch.Generator(device=DEV).manual_seed(14)
+    z = torch.randn(128, 151936, generator=g, device=DEV).mul_(3.0).to(torch.bfloat16)
+    beams = -(torch.rand(32, 4, generator=g, device=DEV) * 6).sort(1).values
+
+    def best_of(scores):
+        times = []
+        for _ in range(12):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            qqe.beam_select(z, scores, 8)
+            b.record()
+            b.synchronize()
+            times.append(a.elapsed_time(b))
+        return sorted(times)[3]
+
+    near = best_of(beams)
+    for score in (-600.0, -1200.0, -5000.0):
+        far = best_of(beams + score)
+        say(f"[beam order] scores of {score}: {far * 1e3:.0f} us, near zero {near * 1e3:.0f} us")
+        assert far < 5 * near
