@@ -51,6 +51,7 @@
 #include <algorithm>
 
 #include "kld_answer.h"
+#include "kld_bins.h"
 
 namespace kldk {
 namespace {
@@ -58,8 +59,6 @@ namespace {
 constexpr int kSlice = 8192;        // tokens of a slice
 constexpr int kScanThreads = 256;
 constexpr int kEach = kSlice / kScanThreads;
-constexpr int kPerUnit = 4;         // bins per binary unit
-constexpr int kBins = 272;          // 64 binary units below the largest weight, and what rounding and bases need
 constexpr int kCopies = 4;          // of the bins in LDS: lanes that add to one bin wait for each other less
 constexpr int kDrawThreads = 512;
 constexpr int kDrawEach = kSlice / kDrawThreads;
@@ -200,21 +199,6 @@ __device__ __forceinline__ Settings settings_of(const SampleArgs& a, int64_t row
 
 // ---- weights ----
 
-// The base of a slice whose largest logit is m: one to two bins above c m, a whole number, so that
-// bases differ by whole numbers. Where c |m| passes 2^45 any other logit lies 2^21 bins or more below
-// m, and the base is c m itself.
-constexpr double kSteep = 0x1p45;
-__device__ __forceinline__ double base_of(float m, double per) {
-    const double at = static_cast<double>(m) * per;
-    return fabs(at) < kSteep ? floor(at) + 2.0 : at;
-}
-// Bins of a logit above the base (at most -1); far below for one that a steep slice drops.
-__device__ __forceinline__ double position(float z, float m, double per, double base) {
-    if (fabs(base) < kSteep) return fma(static_cast<double>(z), per, -base);
-    return z >= m ? -1.0 : -0x1p60;
-}
-constexpr double kLowest = -0.5 - kBins;  // positions from here on have a bin (a NaN, 0 times infinity, has none)
-
 // 2^(r / kPerUnit), |r| <= 1/2, plus 2^(52 - kUnit), whose last place is 2^-kUnit: a polynomial of degree 6
 // that interpolates at Chebyshev's nodes (relative error 1.3e-13), rounded once to whole units. The scan
 // holds its coefficients in scalar registers: left to itself the compiler copies each into vector
@@ -257,7 +241,6 @@ __device__ __forceinline__ double weight(const Raise& raise, double x) {
     const double f = rint(x);
     return (raise(x - f) - kRaised) * scale_of(static_cast<int>(f));
 }
-__device__ __forceinline__ int bin_of(double x) { return -1 - static_cast<int>(rint(x)); }
 
 // The sum of mantissas and the count of a bin's word.
 __device__ __forceinline__ double mass_in(uint64_t word) {
@@ -324,8 +307,7 @@ __global__ void __launch_bounds__(kScanThreads) scan_kernel(SampleArgs a, int64_
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
             const double x = fma(static_cast<double>(z[i]), s.per, -base), f = rint(x);
-            const unsigned int bin = min(static_cast<unsigned int>(~static_cast<int>(f)), static_cast<unsigned int>(kBins));
-            atomicAdd(&bins[bin * kCopies + copy],
+            atomicAdd(&bins[bin_or_none(f) * kCopies + copy],
                       static_cast<unsigned long long>(whole_units(raise(x - f))) + (1ull << kCountAt));
         }
     }
