@@ -7,11 +7,11 @@
 // The token is the first kept one, by ids, at which the running sum of the kept w
 // passes u times the whole.
 //
-// With c = 4 log2 e / T a weight is 2^(c z / 4). It is taken as 2^((f + r) / 4) over a base, f =
-// rint(c z - base) and |r| <= 1/2: 2^(r / 4) is the token's mantissa, rounded to a whole multiple
-// of 2^-36, and f the bin it belongs to, a quarter of a binary unit wide. A base is a whole
-// number near c times the largest logit of a row or slice, so that a slice's bins are the row's,
-// some whole number down. Sums of mantissas in a bin are sums of integers: they depend on no
+// With c = 4 log2 e / T a weight is 2^(c z / 4). It is taken as 2^((f + r) / 4), f = rint(c z) and
+// |r| <= 1/2: 2^(r / 4) is the token's mantissa, rounded to a whole multiple of 2^-36, and f the
+// bin it belongs to, a quarter of a binary unit wide (kld_bins.h). Bins are counted down from
+// that of the largest logit of a row or slice, so that a slice's bins are the row's, some whole
+// number down. Sums of mantissas in a bin are sums of integers: they depend on no
 // order, and their relative error is below 2^-36 whatever the row. Sums over bins are formed in
 // float64 in a fixed order.
 //
@@ -70,17 +70,14 @@ constexpr int kUnit = 36;           // mantissas are whole multiples of 2^-kUnit
 constexpr int kCountAt = 50;        // a bin's word: its sum of mantissas below this bit, its count from it on
 constexpr double kLeast = 0x1p-64;  // smallest share of the likeliest token's weight that is kept
 constexpr int64_t kPassSlices = 32768;  // slices per pass over the workspace (at 19 a row 305 MB)
-constexpr double kLog2e = 1.4426950408889634074;
 // Sums that equal each other but for the order of their additions count as equal.
 constexpr double kSame = 0x1p-44;
 
 // What the scan leaves of a slice, and the plan for its listing.
 struct Info {
-    double base;        // in bins, see base_of
-    double mass;        // where there are no limits: its sum of weights, over that of the base
+    double mass;        // where there are no limits: its sum of weights, over that of its first bin
     unsigned int best;  // order of its largest logit, 0 if none is finite
-    float from, to;     // logits in [from, to) are listed
-    int shift;          // bins between the row's base and this one
+    int listed;         // whether any token of it belongs to the bins that are listed
 };
 struct Token {
     unsigned int order;
@@ -93,8 +90,9 @@ struct Plan {
     double mass[kLaneBins * 64];
     int count[kLaneBins * 64];
     int first, last;
-    int listed;  // tokens so far
-    int unused;
+    float from, to;      // their logits, [from, to)
+    unsigned int best;   // order of the row's largest logit
+    int listed;          // tokens so far
 };
 struct Layout {
     Info* info;              // [rows][slices]
@@ -175,7 +173,7 @@ __device__ __forceinline__ bool allowed(float z) { return z < INFINITY && z > -I
 enum Mode { kGreedy, kNoLimit, kLimited };
 
 struct Settings {
-    double per;    // c, in bins
+    Heat heat;
     int64_t k;     // vocab: no limit
     double p;      // 1: no limit
     double least;  // the least share's logarithm, in bins
@@ -188,7 +186,7 @@ __device__ __forceinline__ Settings settings_of(const SampleArgs& a, int64_t row
     Settings s;
     const double heat = setting(a.temperature, row), p = setting(a.top_p, row), m = setting(a.min_p, row);
     const int k = a.top_ks ? a.top_ks[row] : a.top_k;
-    s.per = heat > 0.0 ? fmin(kPerUnit * kLog2e / heat, 1e200) : 0.0;  // times any logit finite
+    s.heat = heat_of(heat);
     s.k = k > 0 && k < a.vocab ? k : a.vocab;
     s.p = p < 1.0 ? p : 1.0;
     // less a rounding: a weight that float64 rounds to 1 is 1
@@ -235,12 +233,9 @@ __device__ __forceinline__ double scale_of(int f) {
     return ldexp(f & 1 ? half * 0x1.306fe0a31b715p+0 : half, f >> 2);
 }
 // What the units of a bin's mantissas weigh.
-__device__ __forceinline__ double unit_of(int bin) { return ldexp(scale_of(-1 - bin), -kUnit); }
-// 2^(x / kPerUnit) for the positions that have a bin.
-__device__ __forceinline__ double weight(const Raise& raise, double x) {
-    const double f = rint(x);
-    return (raise(x - f) - kRaised) * scale_of(static_cast<int>(f));
-}
+__device__ __forceinline__ double unit_of(int bin) { return ldexp(scale_of(-bin), -kUnit); }
+// The weight of a logit that has a bin.
+__device__ __forceinline__ double weight(const Raise& raise, Spot at) { return (raise(at.r) - kRaised) * scale_of(-at.bin); }
 
 // The sum of mantissas and the count of a bin's word.
 __device__ __forceinline__ double mass_in(uint64_t word) {
@@ -289,27 +284,20 @@ __global__ void __launch_bounds__(kScanThreads) scan_kernel(SampleArgs a, int64_
     for (int i = 0; i < kScanThreads / 64; ++i) m = fmaxf(m, part_max[i]);
     Info* info = out.info + task;
     const bool none = !(m > -INFINITY);
-    const double base = none ? 0.0 : base_of(m, s.per);
     if (none || s.mode == kGreedy) {
-        if (thread == 0) *info = Info{base, 0.0, none ? 0 : order_of(m), 0.0f, 0.0f, 0};
+        if (thread == 0) *info = Info{0.0, none ? 0 : order_of(m), 0};
         return;
     }
     Raise raise;
     raise.hold();
-    const bool steep = !(fabs(base) < kSteep);  // then only logits that equal the largest have a weight
+    const Frame frame = frame_of(m, s.heat);
     // Logits that have no bin go to one behind the others.
-    const int copy = thread & (kCopies - 1);
-    if (steep) {
+    unsigned long long* const mine = bins + (thread & (kCopies - 1));
 #pragma unroll
-        for (int i = 0; i < kEach; ++i)
-            if (z[i] == m) atomicAdd(&bins[copy], static_cast<unsigned long long>(whole_units(raise(0.0))) + (1ull << kCountAt));
-    } else {
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            const double x = fma(static_cast<double>(z[i]), s.per, -base), f = rint(x);
-            atomicAdd(&bins[bin_or_none(f) * kCopies + copy],
-                      static_cast<unsigned long long>(whole_units(raise(x - f))) + (1ull << kCountAt));
-        }
+    for (int i = 0; i < kEach; ++i) {
+        const Spot at = spot_of(z[i], frame);
+        atomicAdd(mine + min(static_cast<unsigned int>(at.bin), static_cast<unsigned int>(kBins)) * kCopies,
+                  static_cast<unsigned long long>(whole_units(raise(at.r))) + (1ull << kCountAt));
     }
     __syncthreads();
     double sum = 0.0;
@@ -327,7 +315,7 @@ __global__ void __launch_bounds__(kScanThreads) scan_kernel(SampleArgs a, int64_
         __syncthreads();
         for (int i = 1; i < kScanThreads / 64; ++i) sum += part_sum[i];
     }
-    if (thread == 0) *info = Info{base, sum, order_of(m), 0.0f, 0.0f, 0};
+    if (thread == 0) *info = Info{sum, order_of(m), 0};
 }
 // mantissas are below 2^(1/8)
 static_assert(kSlice < 1 << (64 - kCountAt) && kSlice * 1.1 < static_cast<double>(1 << (kCountAt - kUnit)), "");
@@ -346,9 +334,8 @@ struct Cut {
 
 struct Shared {
     // of the slices
-    double base[kMaxSlices];
-    float best[kMaxSlices], from[kMaxSlices], to[kMaxSlices];  // largest logit; logits [from, to) are collected
-    int shift[kMaxSlices];                                     // bins between the row's base and the slice's
+    int shift[kMaxSlices];                                     // the row's bin of its largest logit
+    int in_range[kMaxSlices];                                  // whether any token of it is in the range below
     unsigned long long mass[kMaxSlices];                       // kept in the last bin, ties apart
     unsigned int ties[kMaxSlices];
     double kept[kMaxSlices];
@@ -360,6 +347,7 @@ struct Shared {
     unsigned int few[kFew];
     int few_count;
     unsigned int least, most;
+    float from, to;      // the range of logits that is looked at, [from, to)
     Cut cut;
     int slice;           // that holds the draw,
     double rest, total;  // what is left of it there, and the sum of all kept
@@ -458,8 +446,7 @@ struct Row {
     int vocab;
     int slices;
     Settings s;
-    float best;   // the largest logit
-    double base;  // its base
+    Frame frame;  // by the largest logit
     const uint64_t* bins;  // of its slices
     const Token* list;     // of its bins list_first to list_last
     int listed;
@@ -495,28 +482,22 @@ struct Row {
         const unsigned int w[4] = {q.x, q.y, q.z, q.w};
         return Elem<E>::get(w, e % Elem<E>::kPer);
     }
-    __device__ __forceinline__ double at(float z) const { return position(z, best, s.per, base); }
+    __device__ __forceinline__ Spot at(float z) const { return spot_of(z, frame); }
     // Whether a token passes min-p.
     __device__ __forceinline__ bool enough(float z) const {
-        return (static_cast<double>(z) - static_cast<double>(best)) * s.per >= s.least;
+        return (static_cast<double>(z) - static_cast<double>(frame.most)) * s.heat.per >= s.least;
     }
-    // The row's bin of a logit of a slice, as the scan had it; kBins or more if it has none.
-    __device__ __forceinline__ int bin_in(int slice, float z) const {
-        const double x = position(z, sh.best[slice], s.per, sh.base[slice]);
-        return x >= kLowest ? bin_of(fmin(x, 0.0)) + sh.shift[slice] : kBins;
-    }
-    // For each slice the logits of the row's bins first to last: [from, to). Bins fall as logits rise.
+    // The logits of bins first to last, [from, to), and the slices that hold any. Bins fall as logits rise.
     __device__ __forceinline__ void set_range(int first, int last) const {
-        const double heat = 1.0 / s.per;
         __syncthreads();
-        for (int t = threadIdx.x; t < 2 * slices; t += kDrawThreads) {
-            const int slice = t >> 1, bin = t & 1 ? first - 1 : last;
-            // the lowest logit whose bin is `bin` or one before it; infinity if there is none. It is next to
-            // where c z reaches the bin's edge, unless c is too small or too large for that to be told.
+        if (threadIdx.x < 2) {
+            const int bin = threadIdx.x == 0 ? last : first - 1;
+            // the lowest logit whose bin is `bin` or one before it. It is next to where c z reaches the
+            // bin's edge, unless c is too small or too large for that to be told.
             unsigned int below = order_of(-INFINITY), above = order_of(INFINITY);
-            if (sh.shift[slice] <= bin) {
-                const auto reaches = [&](unsigned int o) { return bin_in(slice, value_of(o)) <= bin; };
-                const float near = static_cast<float>((sh.base[slice] + sh.shift[slice] - bin - 1.5) * heat);
+            const auto reaches = [&](unsigned int o) { return bin_of(value_of(o), frame) <= bin; };
+            if (bin >= 0) {  // before the first there is none: infinity
+                const float near = static_cast<float>((frame.top - kWhole - bin - 0.5) * (1.0 / frame.per));
                 if (fabsf(near) < 1e30f && fabsf(near) > 1e-30f) {
                     const unsigned int o = order_of(near);
                     if (reaches(o + 2)) above = o + 2;
@@ -530,28 +511,26 @@ struct Row {
                     else below = middle;
                 }
             }
-            float edge = value_of(above);
-            // a slice without tokens in the range is not looked at
-            const int local = last - sh.shift[slice];
-            const bool some = first == last ? local >= 0 && count_of(bins[static_cast<int64_t>(slice) * kBins + local]) != 0
-                                            : bin_in(slice, sh.best[slice]) <= last;
-            if (!some) edge = INFINITY;
-            (t & 1 ? sh.to : sh.from)[slice] = edge;
+            (threadIdx.x == 0 ? sh.from : sh.to) = value_of(above);
+        }
+        for (int i = threadIdx.x; i < slices; i += kDrawThreads) {
+            const int local = last - sh.shift[i];
+            sh.in_range[i] = local >= 0 && (first < last || count_of(bins[static_cast<int64_t>(i) * kBins + local]) != 0);
         }
         __syncthreads();
     }
     __device__ __forceinline__ int next_in_range(int i) const {
         do ++i;
-        while (i < slices && !(sh.from[i] < sh.to[i]));
+        while (i < slices && !sh.in_range[i]);
         return i;
     }
     // f(order, slice) for the tokens in the range set last, out of the row.
     template <class F>
     __device__ __forceinline__ void each_in_range(F f) const {
+        const float from = sh.from, to = sh.to;
 #pragma unroll 1
         for (int i = next_in_range(-1); i < slices; i = next_in_range(i)) {
             const Raw raw = read(i);
-            const float from = sh.from[i], to = sh.to[i];
             unsigned int in = 0;
 #pragma unroll
             for (int e = 0; e < kDrawEach; ++e) {
@@ -585,13 +564,13 @@ struct Row {
         };
         const double unit = unit_of(bin);  // sums are in whole units of the bin
         const double want = want_mass * (1.0 - kSame);
-        const auto units = [&](unsigned int o) __attribute__((always_inline)) { return whole_units(raise(at(value_of(o)) + (1 + bin))); };
+        const auto units = [&](unsigned int o) __attribute__((always_inline)) { return whole_units(raise(at(value_of(o)).r)); };
         const int thread = threadIdx.x, lane = thread & 63;
         unsigned int lo = 0, hi = ~0u;
         int down = -1;  // -1: by weight
         const auto part_of = [&](unsigned int o) __attribute__((always_inline)) {  // the largest logits first
             if (down >= 0) return kSplit - 1 - static_cast<int>((o - lo) >> down);
-            const int part = static_cast<int>((0.5 - (at(value_of(o)) + (1 + bin))) * kSplit);
+            const int part = static_cast<int>((0.5 - at(value_of(o)).r) * kSplit);
             return max(0, min(kSplit - 1, part));
         };
         int above = 0;
@@ -670,10 +649,10 @@ struct Row {
         }
     }
     // Adds a token of a bin to what its slice keeps of it; ties are counted apart.
-    __device__ __forceinline__ void keep(int bin, bool cut_bin, Cut c, bool by_least, bool ties_pass, unsigned int o, int slice) const {
+    __device__ __forceinline__ void keep(bool cut_bin, Cut c, bool by_least, bool ties_pass, unsigned int o, int slice) const {
         const float z = value_of(o);
         if ((!cut_bin || o > c.order) && (!by_least || enough(z)))
-            atomicAdd(&sh.mass[slice], static_cast<unsigned long long>(whole_units(raise(at(z) + (1 + bin)))));
+            atomicAdd(&sh.mass[slice], static_cast<unsigned long long>(whole_units(raise(at(z).r))));
         else if (ties_pass && o == c.order) atomicAdd(&sh.ties[slice], 1u);
     }
 };
@@ -694,22 +673,20 @@ __device__ __forceinline__ bool open_row(Row<E>& r, const Info* info, int* greed
     best = wave_most(best);
     *greedy = -1;
     if (best == 0) return false;
-    r.best = value_of(best);
+    r.frame = frame_of(value_of(best), r.s.heat);
+    r.frame = Frame{from_lane(r.frame.per, 0), from_lane(r.frame.top, 0), from_lane(r.frame.low, 0), r.frame.most};  // scalar registers
     if (r.s.mode == kGreedy) {
         *greedy = static_cast<int>(~wave_most(mine == best ? holder : 0));
         return false;
     }
-    r.base = base_of(r.best, r.s.per);
     for (int i = thread; i < r.slices; i += kDrawThreads) {
         const Info x = info[i];
-        const bool some = x.best != 0 && r.base - x.base < kBins;
-        sh.base[i] = x.base;
-        sh.best[i] = x.best != 0 ? value_of(x.best) : -INFINITY;
-        sh.shift[i] = some ? static_cast<int>(r.base - x.base) : kBins;
+        const float most = x.best != 0 ? value_of(x.best) : -INFINITY;
+        const int shift = bin_of(most, r.frame);
+        sh.shift[i] = shift;
         sh.mass[i] = 0;
         sh.ties[i] = 0;
-        if (r.s.mode == kNoLimit)
-            sh.kept[i] = some && r.enough(value_of(x.best)) ? x.mass * scale_of(-static_cast<int>(r.base - x.base)) : 0.0;
+        if (r.s.mode == kNoLimit) sh.kept[i] = shift < kBins && r.enough(most) ? x.mass * scale_of(-shift) : 0.0;
     }
     __syncthreads();
     return true;
@@ -760,10 +737,10 @@ __device__ __forceinline__ Place bin_of_limit(const Shared& sh, int limit, int k
     }
     return first_reached(n, w, [&](int count, double mass) { return count >= k || mass >= p * (1.0 - kSame); });
 }
-// min-p as a position, and the bin it falls in.
+// The bin that min-p falls in.
 template <class E>
 __device__ __forceinline__ int bin_of_least(const Row<E>& r) {
-    return bin_of(fmax(r.at(r.best) + r.s.least, kLowest));
+    return min(kBins - 1, -static_cast<int>(rint(r.at(r.frame.most).r + r.s.least)));
 }
 // Where the tokens of a bin are listed those of earlier ones may be too: with top-p to come behind top-k its
 // bin is among them.
@@ -780,7 +757,7 @@ template <class E>
 __device__ __forceinline__ Row<E> row_of(const SampleArgs& a, const Layout& ws, int64_t row, int64_t here, int slices,
                                          Shared& sh) {
     return Row<E>{static_cast<const E*>(a.logits) + row * a.row_stride, static_cast<int>(a.vocab), slices,
-                  settings_of(a, row), 0.0f, 0.0, ws.bins + here * slices * kBins, ws.list + here * kList, 0, Raise(), sh};
+                  settings_of(a, row), Frame{}, ws.bins + here * slices * kBins, ws.list + here * kList, 0, Raise(), sh};
 }
 
 // The bin in which a row is cut first, and for each of its slices the logits that belong to it.
@@ -818,9 +795,16 @@ __global__ void __launch_bounds__(kDrawThreads) plan_kernel(SampleArgs a, int64_
     if (listed) {
         r.set_range(first, at.at);
         for (int i = thread; i < slices; i += kDrawThreads)
-            info[i].from = sh.from[i], info[i].to = sh.to[i], info[i].shift = sh.shift[i];
+            info[i].listed = sh.in_range[i];
     }
-    if (thread == 0) plan->first = first, plan->last = listed ? at.at : -1, plan->listed = 0;
+    if (thread == 0) {
+        plan->first = first;
+        plan->last = listed ? at.at : -1;
+        plan->from = sh.from;
+        plan->to = sh.to;
+        plan->best = order_of(r.frame.most);
+        plan->listed = 0;
+    }
 }
 
 // The tokens that belong to it, a slice per workgroup. Eight waves to a SIMD: 48 us for 1024 x 151936 bfloat16, with
@@ -830,10 +814,10 @@ __global__ void __launch_bounds__(kScanThreads, 8) list_kernel(SampleArgs a, int
     const int64_t task = blockIdx.x, here = task / slices, row = first_row + here;
     const int slice = static_cast<int>(task % slices), thread = threadIdx.x, lane = thread & 63;
     Plan* plan = ws.plan + here;
-    const int first = plan->first, last = plan->last;
-    if (last < 0) return;
-    const Info info = ws.info[task];
-    if (!(info.from < info.to)) return;
+    const int first = plan->first, last = plan->last, some = ws.info[task].listed;
+    const float from = plan->from, below = plan->to;
+    const unsigned int best = plan->best;
+    if (last < 0 || !some) return;
     const E* in = static_cast<const E*>(a.logits) + row * a.row_stride;
     const int vocab = static_cast<int>(a.vocab);
     float z[kEach];
@@ -842,20 +826,21 @@ __global__ void __launch_bounds__(kScanThreads, 8) list_kernel(SampleArgs a, int
     static_assert(kEach == 32, "");
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
-        mine |= static_cast<unsigned int>(z[i] >= info.from && z[i] < info.to) << i;
+        mine |= static_cast<unsigned int>(z[i] >= from && z[i] < below) << i;
     }
     if (!__ballot(mine != 0)) return;
     const int n = __popc(mine), to = wave_sum_to(n);
     int put = 0;
     if (lane == 63) put = atomicAdd(&plan->listed, to);
     put = from_lane(put, 63) + to - n;
-    const double per = settings_of(a, row).per, base = base_of(value_of(info.best), per);
+    Frame frame{};
+    if (first < last) frame = frame_of(value_of(best), settings_of(a, row).heat);
     Token* list = ws.list + here * kList;
     // a lane has few: they are read again rather than picked out of registers
     for (; mine; mine &= mine - 1, ++put) {
         const int id = held_id<E>(slice, vocab, __builtin_ctz(mine));
         const float z = Elem<E>::widen(in[id]);
-        const int bin = first < last ? bin_of(position(z, value_of(info.best), per, base)) + info.shift : last;
+        const int bin = first < last ? spot_of(z, frame).bin : last;
         if (put < kList) list[put] = Token{order_of(z), static_cast<unsigned int>(id) << 9 | bin};
     }
 }
@@ -885,7 +870,7 @@ __global__ void __launch_bounds__(kDrawThreads, 4) draw_kernel(SampleArgs a, int
         unsigned int at = ~0u;
 #pragma unroll
         for (int e = kDrawEach - 1; e >= 0; --e)
-            if (allowed(r.get(raw, e)) && r.get(raw, e) == r.best) at = r.id_of(greedy, e);
+            if (allowed(r.get(raw, e)) && r.get(raw, e) == r.frame.most) at = r.id_of(greedy, e);
         if (at != ~0u) atomicMin(&sh.least, at);
         __syncthreads();
         if (thread == 0) finish(static_cast<int>(sh.least), 0.0);
@@ -941,7 +926,7 @@ __global__ void __launch_bounds__(kDrawThreads, 4) draw_kernel(SampleArgs a, int
                 const bool by_least = last_bin == bin_least;
                 const bool ties_pass = cut_bin && (!by_least || r.enough(value_of(cut.order)));
                 r.each_of(bin, in_list, [&](unsigned int o, int slice) __attribute__((always_inline)) {
-                    r.keep(bin, cut_bin, cut, by_least, ties_pass, o, slice);
+                    r.keep(cut_bin, cut, by_least, ties_pass, o, slice);
                 });
             }
         }
@@ -1004,9 +989,6 @@ __global__ void __launch_bounds__(kDrawThreads, 4) draw_kernel(SampleArgs a, int
     __syncthreads();
     const int slice = sh.slice, take = static_cast<int>(sh.ties[slice]);
     const double rest = sh.rest, total = sh.total;
-    const int down = sh.shift[slice];
-    const float m = sh.best[slice];
-    const double from = sh.base[slice];
 
     // In that slice the token: each thread has kDrawEach consecutive ones, in LDS (its own place, so that a loop
     // over them is short).
@@ -1022,16 +1004,15 @@ __global__ void __launch_bounds__(kDrawThreads, 4) draw_kernel(SampleArgs a, int
     int seen = seen_before;
     const auto kept = [&](int e) __attribute__((always_inline)) {
         const float mine = z[e * kDrawThreads];
-        const double x = position(mine, m, s.per, from);
-        if (!allowed(mine) || !(x >= kLowest)) return 0.0;
-        const int bin = bin_of(x) + down;
-        if (bin > last_bin) return 0.0;
-        if (bin == last_bin) {
+        if (!(mine < INFINITY)) return 0.0;
+        const Spot at = r.at(mine);
+        if (at.bin > last_bin) return 0.0;
+        if (at.bin == last_bin) {
             const unsigned int o = order_of(mine);
             if (cut_bin && (o < cut.order || (o == cut.order && seen++ >= take))) return 0.0;
             if (last_bin == bin_least && !r.enough(mine)) return 0.0;
         }
-        return weight(r.raise, x - down);
+        return weight(r.raise, at);
     };
     double sum = 0.0;
 #pragma unroll 1
