@@ -626,7 +626,7 @@ kld_status kld_eval_matmul_int8(const int8_t* x, int64_t x_stride, const float* 
  * The token is the first kept one, in order of ids, at which the running sum of
  * the kept w exceeds uniforms[r] times their whole sum; logp is the logarithm of
  * w over that sum, the log-probability with which it was drawn. Weights are formed
- * in float64 and rounded to 2^-36 of themselves, sums of them are exact or in float64,
+ * in float64 and rounded to 2^-45 of themselves, sums of them are exact or in float64,
  * and a sum that equals a border but for that counts as reaching it.
  *   logits       device rows of `vocab` elements of dtype, row_stride elements
  *                apart (>= vocab); any alignment of the type; vocab and n_rows at most 4,194,304

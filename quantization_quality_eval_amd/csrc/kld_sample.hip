@@ -8,17 +8,17 @@
 // passes u times the whole.
 //
 // With c = 4 log2 e / T a weight is 2^(c z / 4). It is taken as 2^((f + r) / 4), f = rint(c z) and
-// |r| <= 1/2: 2^(r / 4) is the token's mantissa, rounded to a whole multiple of 2^-36, and f the
+// |r| <= 1/2: 2^(r / 4) is the token's mantissa, rounded to a whole multiple of 2^-45, and f the
 // bin it belongs to, a quarter of a binary unit wide (kld_bins.h). Bins are counted down from
 // that of the largest logit of a row or slice, so that a slice's bins are the row's, some whole
 // number down. Sums of mantissas in a bin are sums of integers: they depend on no
-// order, and their relative error is below 2^-36 whatever the row. Sums over bins are formed in
+// order, and their relative error is below 2^-45 whatever the row. Sums over bins are formed in
 // float64 in a fixed order.
 //
 // Launches, over as many rows as the workspace holds (a slice is 8192 tokens):
 //   scan  a workgroup per slice: its largest logit, and the count and the sum of mantissas of
 //         each of its upper 272 bins (68 binary units; what lies below 2^-64 of the largest
-//         weight is dropped), both in one 64-bit word that LDS atomics add to;
+//         weight is dropped), by LDS atomics;
 //   plan  a workgroup per row: adds the slices' bins up, finds the bin in which the order is
 //         cut first, and for each slice the logits that belong to that bin, by bisection;
 //   list  a workgroup per slice: the tokens between those logits, compared as floats, to a
@@ -59,15 +59,13 @@ namespace {
 constexpr int kSlice = 8192;        // tokens of a slice
 constexpr int kScanThreads = 256;
 constexpr int kEach = kSlice / kScanThreads;
-constexpr int kCopies = 4;          // of the bins in LDS: lanes that add to one bin wait for each other less
+constexpr int kCopies = 8;          // of the bins in LDS: lanes that add to one bin wait for each other less
 constexpr int kDrawThreads = 512;
 constexpr int kDrawEach = kSlice / kDrawThreads;
 constexpr int kList = 16384;        // tokens of a row that are listed
 constexpr int kSplit = 256;         // parts of a bin, or of a range of logits
 constexpr int kFew = 64;            // tokens that a wave ranks
 constexpr int kMaxSlices = 512;     // of a row: what the draw knows of each is held in LDS
-constexpr int kUnit = 36;           // mantissas are whole multiples of 2^-kUnit
-constexpr int kCountAt = 50;        // a bin's word: its sum of mantissas below this bit, its count from it on
 constexpr double kLeast = 0x1p-64;  // smallest share of the likeliest token's weight that is kept
 constexpr int64_t kPassSlices = 32768;  // slices per pass over the workspace (at 19 a row 305 MB)
 // Sums that equal each other but for the order of their additions count as equal.
@@ -98,10 +96,11 @@ struct Layout {
     Info* info;              // [rows][slices]
     Plan* plan;              // [rows]
     Token* list;             // [rows][kList]
-    uint64_t* bins;          // [rows][slices][kBins]: words
+    double* masses;          // [rows][slices][kBins]: a bin's sum of mantissas, in units
+    uint16_t* counts;        // and its count
 };
 __host__ __device__ inline int64_t slices_of(int64_t vocab) { return (vocab + kSlice - 1) / kSlice; }
-constexpr int64_t kSliceBytes = sizeof(Info) + kBins * sizeof(uint64_t);
+constexpr int64_t kSliceBytes = sizeof(Info) + kBins * (sizeof(double) + sizeof(uint16_t));
 constexpr int64_t kRowBytes = sizeof(Plan) + kList * sizeof(Token);
 
 template <class E>
@@ -197,51 +196,16 @@ __device__ __forceinline__ Settings settings_of(const SampleArgs& a, int64_t row
 
 // ---- weights ----
 
-// 2^(r / kPerUnit), |r| <= 1/2, plus 2^(52 - kUnit), whose last place is 2^-kUnit: a polynomial of degree 6
-// that interpolates at Chebyshev's nodes (relative error 1.3e-13), rounded once to whole units. The scan
-// holds its coefficients in scalar registers: left to itself the compiler copies each into vector
-// registers before its step.
-struct Raise {
-    double c[7];
-    __device__ __forceinline__ Raise()
-        : c{65537.0,
-            0x1.62e42fefb19e3p-3,
-            0x1.ebfbdff83132cp-7,
-            0x1.c6b08bb064223p-11,
-            0x1.3b2ab6606b782p-15,
-            0x1.5da3fc8f86d44p-20,
-            0x1.431c79fd8ebd8p-25} {}
-    __device__ __forceinline__ void hold() {
+// The scan holds the polynomial's coefficients in scalar registers: left to itself the compiler copies each into
+// vector registers before its step.
+__device__ __forceinline__ void hold(Raise& raise) {
 #pragma unroll
-        for (int i = 0; i < 7; ++i) asm volatile("" : "+s"(c[i]));
-    }
-    __device__ __forceinline__ double operator()(double r) const {
-        double s = c[6];
-#pragma unroll
-        for (int i = 5; i >= 0; --i) s = fma(s, r, c[i]);
-        return s;
-    }
-};
-static_assert(52 - kUnit == 16 && kPerUnit == 4, "Raise adds 2^16, of quarters");
-constexpr double kRaised = 65536.0;
-__device__ __forceinline__ uint64_t whole_units(double raised_r) {
-    return static_cast<uint64_t>(__double_as_longlong(raised_r) - __double_as_longlong(kRaised));
-}
-// 2^(f / kPerUnit) for whole f.
-__device__ __forceinline__ double scale_of(int f) {
-    const double half = f & 2 ? 0x1.6a09e667f3bcdp+0 : 1.0;
-    return ldexp(f & 1 ? half * 0x1.306fe0a31b715p+0 : half, f >> 2);
+    for (int i = 0; i <= Raise::kDegree; ++i) asm volatile("" : "+s"(raise.c[i]));
 }
 // What the units of a bin's mantissas weigh.
 __device__ __forceinline__ double unit_of(int bin) { return ldexp(scale_of(-bin), -kUnit); }
 // The weight of a logit that has a bin.
-__device__ __forceinline__ double weight(const Raise& raise, Spot at) { return (raise(at.r) - kRaised) * scale_of(-at.bin); }
-
-// The sum of mantissas and the count of a bin's word.
-__device__ __forceinline__ double mass_in(uint64_t word) {
-    return static_cast<double>(word & ((uint64_t{1} << kCountAt) - 1));
-}
-__device__ __forceinline__ int count_of(uint64_t word) { return static_cast<int>(word >> kCountAt); }
+__device__ __forceinline__ double weight(const Raise& raise, Spot at) { return mantissa_of(raise(at.r)) * scale_of(-at.bin); }
 
 // ---- the scan ----
 
@@ -261,14 +225,10 @@ __global__ void __launch_bounds__(kScanThreads) scan_kernel(SampleArgs a, int64_
     const Settings s = settings_of(a, row);
     if (s.mode != kGreedy)
         for (int i = thread; i < kBins * kCopies; i += kScanThreads) bins[i] = 0;
-    bool clean = true;
     float m = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-        clean = clean && z[i] < INFINITY;
-        m = fmaxf(m, z[i]);
-    }
-    if (!clean) {
+    for (int i = 0; i < kEach; ++i) m = __builtin_elementwise_maximum(m, z[i]);  // a NaN where any is
+    if (!(m < INFINITY)) {
         m = -INFINITY;
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
@@ -289,24 +249,34 @@ __global__ void __launch_bounds__(kScanThreads) scan_kernel(SampleArgs a, int64_
         return;
     }
     Raise raise;
-    raise.hold();
+    hold(raise);
     const Frame frame = frame_of(m, s.heat);
     // Logits that have no bin go to one behind the others.
-    unsigned long long* const mine = bins + (thread & (kCopies - 1));
+    const int copy = thread & (kCopies - 1);
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
         const Spot at = spot_of(z[i], frame);
-        atomicAdd(mine + min(static_cast<unsigned int>(at.bin), static_cast<unsigned int>(kBins)) * kCopies,
-                  static_cast<unsigned long long>(whole_units(raise(at.r))) + (1ull << kCountAt));
+        atomicAdd(&bins[min(static_cast<unsigned int>(at.bin), static_cast<unsigned int>(kBins)) * kCopies + copy],
+                  __builtin_bit_cast(unsigned long long, raise(at.r)));
     }
     __syncthreads();
     double sum = 0.0;
     for (int i = thread; i < kBins; i += kScanThreads) {
-        uint64_t word = 0;
+        uint64_t units = 0;
+        int count = 0;
 #pragma unroll
-        for (int c = 0; c < kCopies; ++c) word += bins[i * kCopies + c];
-        if (s.mode == kLimited) out.bins[task * kBins + i] = word;
-        else sum += mass_in(word) * unit_of(i);
+        for (int c = 0; c < kCopies; ++c) {
+            const uint64_t word = bins[i * kCopies + c];
+            units += units_in(word);
+            count += count_in(word);
+        }
+        const double mass = static_cast<double>(units);
+        if (s.mode == kLimited) {
+            out.masses[task * kBins + i] = mass;
+            out.counts[task * kBins + i] = static_cast<uint16_t>(count);
+        } else {
+            sum += mass * unit_of(i);
+        }
     }
     if (s.mode == kNoLimit) {
 #pragma unroll
@@ -317,8 +287,7 @@ __global__ void __launch_bounds__(kScanThreads) scan_kernel(SampleArgs a, int64_
     }
     if (thread == 0) *info = Info{sum, order_of(m), 0};
 }
-// mantissas are below 2^(1/8)
-static_assert(kSlice < 1 << (64 - kCountAt) && kSlice * 1.1 < static_cast<double>(1 << (kCountAt - kUnit)), "");
+static_assert(kSlice / kCopies <= kWordTokens && kScanThreads % kCopies == 0 && kSlice < 1 << 16, "");
 
 // ---- the draw ----
 
@@ -332,6 +301,11 @@ struct Cut {
     double mass;
 };
 
+// Of the words in which a cut sums a part, up to a whole row's tokens: 52 and 64 bits.
+constexpr int kLowBits = 19, kCountAt = 41;
+static_assert(kSampleMaxVocab <= int64_t{1} << 22 && kSampleMaxVocab < int64_t{1} << (64 - kCountAt) && 22 + kLowBits <= kCountAt &&
+              kUnit + 1 - kLowBits + 22 <= 53, "");
+
 struct Shared {
     // of the slices
     int shift[kMaxSlices];                                     // the row's bin of its largest logit
@@ -342,8 +316,7 @@ struct Shared {
     // the row's bins
     double bin_mass[kLaneBins * 64];
     int bin_count[kLaneBins * 64];
-    unsigned long long split_mass[kSplit];
-    unsigned int split_count[kSplit];
+    unsigned long long split_high[kSplit], split_low[kSplit];
     unsigned int few[kFew];
     int few_count;
     unsigned int least, most;
@@ -387,6 +360,9 @@ __device__ __forceinline__ unsigned int from_lane(unsigned int x, int lane) {
     return static_cast<unsigned int>(__builtin_amdgcn_readlane(static_cast<int>(x), lane));
 }
 __device__ __forceinline__ int from_lane(int x, int lane) { return __builtin_amdgcn_readlane(x, lane); }
+__device__ __forceinline__ uint64_t from_lane(uint64_t x, int lane) {
+    return static_cast<uint64_t>(from_lane(static_cast<unsigned int>(x >> 32), lane)) << 32 | from_lane(static_cast<unsigned int>(x), lane);
+}
 __device__ __forceinline__ double from_lane(double x, int lane) {
     return __hiloint2double(from_lane(__double2hiint(x), lane), from_lane(__double2loint(x), lane));
 }
@@ -447,7 +423,8 @@ struct Row {
     int slices;
     Settings s;
     Frame frame;  // by the largest logit
-    const uint64_t* bins;  // of its slices
+    const double* masses;    // of its slices' bins
+    const uint16_t* counts;
     const Token* list;     // of its bins list_first to list_last
     int listed;
     Raise raise;
@@ -515,7 +492,7 @@ struct Row {
         }
         for (int i = threadIdx.x; i < slices; i += kDrawThreads) {
             const int local = last - sh.shift[i];
-            sh.in_range[i] = local >= 0 && (first < last || count_of(bins[static_cast<int64_t>(i) * kBins + local]) != 0);
+            sh.in_range[i] = local >= 0 && (first < last || counts[static_cast<int64_t>(i) * kBins + local] != 0);
         }
         __syncthreads();
     }
@@ -564,7 +541,9 @@ struct Row {
         };
         const double unit = unit_of(bin);  // sums are in whole units of the bin
         const double want = want_mass * (1.0 - kSame);
-        const auto units = [&](unsigned int o) __attribute__((always_inline)) { return whole_units(raise(at(value_of(o)).r)); };
+        const auto units = [&](unsigned int o) __attribute__((always_inline)) { return units_of(raise(at(value_of(o)).r)); };
+        // A part's mantissas are summed in two words, without their last bits and those alone below a count of them.
+        const auto count_of = [&](int part) __attribute__((always_inline)) { return static_cast<int>(sh.split_low[part] >> kCountAt); };
         const int thread = threadIdx.x, lane = thread & 63;
         unsigned int lo = 0, hi = ~0u;
         int down = -1;  // -1: by weight
@@ -577,14 +556,15 @@ struct Row {
         double above_mass = 0.0;
         for (;;) {
             __syncthreads();
-            if (thread < kSplit) sh.split_count[thread] = 0, sh.split_mass[thread] = 0;
+            if (thread < kSplit) sh.split_high[thread] = 0, sh.split_low[thread] = 0;
             if (thread == 0) sh.few_count = 0, sh.least = ~0u, sh.most = 0;
             __syncthreads();
             each([&](unsigned int o) __attribute__((always_inline)) {
                 if (o < lo || o > hi) return;
                 const int part = part_of(o);
-                atomicAdd(&sh.split_count[part], 1u);
-                atomicAdd(&sh.split_mass[part], static_cast<unsigned long long>(units(o)));
+                const unsigned long long u = units(o);
+                atomicAdd(&sh.split_high[part], u >> kLowBits);
+                atomicAdd(&sh.split_low[part], (u & ((1ull << kLowBits) - 1)) + (1ull << kCountAt));
             });
             __syncthreads();
             constexpr int kOf = kSplit / 64;
@@ -592,13 +572,14 @@ struct Row {
             double w[kOf];
 #pragma unroll
             for (int i = 0; i < kOf; ++i) {
-                n[i] = sh.split_count[lane * kOf + i];
-                w[i] = static_cast<double>(sh.split_mass[lane * kOf + i]) * unit;
+                n[i] = count_of(lane * kOf + i);
+                const double low = static_cast<double>(sh.split_low[lane * kOf + i] & ((1ull << kCountAt) - 1));
+                w[i] = fma(static_cast<double>(sh.split_high[lane * kOf + i]), 1 << kLowBits, low) * unit;
             }
             const Place found = first_reached(n, w, [&](int count, double mass) {
                 return above + count >= want_count || above_mass + mass >= want;
             });
-            const int in_part = static_cast<int>(sh.split_count[max(found.at, 0)]);
+            const int in_part = count_of(max(found.at, 0));
             above += found.count;
             above_mass += found.mass;
             const bool few = in_part <= kFew;
@@ -618,20 +599,20 @@ struct Row {
             if (thread < 64) {
                 // each lane's token: how many there are above it and what they weigh, how many equal it
                 const unsigned int mine = few ? (lane < in_part ? sh.few[lane] : 0) : lane == 0 ? sh.least : 0;
-                const double weighs = mine != 0 ? static_cast<double>(units(mine)) : 0.0;
+                const uint64_t weighs = mine != 0 ? units(mine) : 0;
                 int before = 0, same = few ? 0 : in_part;
-                double before_units = 0.0;  // whole numbers below 2^53: exact in any order
+                uint64_t before_units = 0;
                 if (few)
 #pragma unroll 1
                     for (int i = 0; i < in_part; ++i) {
                         const unsigned int o = from_lane(mine, i);
-                        const double u = from_lane(weighs, i);
+                        const uint64_t u = from_lane(weighs, i);
                         before += o > mine;
-                        before_units += o > mine ? u : 0.0;
+                        before_units += o > mine ? u : 0;
                         same += o == mine;
                     }
                 const int count = above + before;
-                const double mass = above_mass + before_units * unit, each_mass = weighs * unit;
+                const double mass = above_mass + static_cast<double>(before_units) * unit, each_mass = static_cast<double>(weighs) * unit;
                 // the first logit that reaches it, or (a rounding short) the last
                 const bool reached = count + same >= want_count || mass + same * each_mass >= want;
                 const unsigned int first = wave_most(mine != 0 && reached ? mine : 0);
@@ -652,7 +633,7 @@ struct Row {
     __device__ __forceinline__ void keep(bool cut_bin, Cut c, bool by_least, bool ties_pass, unsigned int o, int slice) const {
         const float z = value_of(o);
         if ((!cut_bin || o > c.order) && (!by_least || enough(z)))
-            atomicAdd(&sh.mass[slice], static_cast<unsigned long long>(whole_units(raise(at(z).r))));
+            atomicAdd(&sh.mass[slice], static_cast<unsigned long long>(units_of(raise(at(z).r))));
         else if (ties_pass && o == c.order) atomicAdd(&sh.ties[slice], 1u);
     }
 };
@@ -702,9 +683,11 @@ __device__ __forceinline__ void add_bins(const Row<E>& r) {
 #pragma unroll 8
             for (int i = 0; i < r.slices; ++i) {
                 const int at = thread - r.sh.shift[i];
-                const uint64_t word = at >= 0 ? r.bins[static_cast<int64_t>(i) * kBins + at] : 0;
-                mass += mass_in(word);
-                count += count_of(word);
+                const int64_t from = static_cast<int64_t>(i) * kBins + max(at, 0);  // read in any case: no branches
+                const double w = r.masses[from];
+                const int n = r.counts[from];
+                mass += at >= 0 ? w : 0.0;
+                count += at >= 0 ? n : 0;
             }
         }
         r.sh.bin_mass[thread] = mass * unit_of(thread);
@@ -757,7 +740,7 @@ template <class E>
 __device__ __forceinline__ Row<E> row_of(const SampleArgs& a, const Layout& ws, int64_t row, int64_t here, int slices,
                                          Shared& sh) {
     return Row<E>{static_cast<const E*>(a.logits) + row * a.row_stride, static_cast<int>(a.vocab), slices,
-                  settings_of(a, row), Frame{}, ws.bins + here * slices * kBins, ws.list + here * kList, 0, Raise(), sh};
+                  settings_of(a, row), Frame{}, ws.masses + here * slices * kBins, ws.counts + here * slices * kBins, ws.list + here * kList, 0, Raise(), sh};
 }
 
 // The bin in which a row is cut first, and for each of its slices the logits that belong to it.
@@ -852,7 +835,7 @@ __global__ void __launch_bounds__(kDrawThreads, 4) draw_kernel(SampleArgs a, int
     const int64_t here = blockIdx.x, row = first_row + here;
     const int thread = threadIdx.x, lane = thread & 63, wave = thread >> 6;
     Row<E> r = row_of<E>(a, ws, row, here, slices, sh);
-    r.raise.hold();
+    hold(r.raise);
     const Settings& s = r.s;
     const auto finish = [&](int token, double logp) {
         a.tokens_out[row] = token;
@@ -936,7 +919,7 @@ __global__ void __launch_bounds__(kDrawThreads, 4) draw_kernel(SampleArgs a, int
             const int down = sh.shift[i];
             double above = 0.0;
             for (int b = lane; b + down < last_bin; b += 64)
-                above += mass_in(r.bins[static_cast<int64_t>(i) * kBins + b]) * unit_of(b + down);
+                above += r.masses[static_cast<int64_t>(i) * kBins + b] * unit_of(b + down);
 #pragma unroll
             for (int o = 32; o >= 1; o >>= 1) above += __shfl_xor(above, o);
             if (lane == 0) sh.kept[i] = above;
@@ -1056,7 +1039,8 @@ hipError_t launch(const SampleArgs& a, void* workspace, hipStream_t stream) {
     ws.info = static_cast<Info*>(workspace);
     ws.plan = reinterpret_cast<Plan*>(ws.info + rows * slices);
     ws.list = reinterpret_cast<Token*>(ws.plan + rows);
-    ws.bins = reinterpret_cast<uint64_t*>(ws.list + rows * kList);
+    ws.masses = reinterpret_cast<double*>(ws.list + rows * kList);
+    ws.counts = reinterpret_cast<uint16_t*>(ws.masses + rows * slices * kBins);
     const bool limits = a.temperature.each || a.top_ks || a.top_p.each || a.min_p.each ||
                         (a.temperature.all > 0.0 &&
                          ((a.top_k > 0 && a.top_k < a.vocab) || a.top_p.all < 1.0 || a.min_p.all > kLeast));

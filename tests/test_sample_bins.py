@@ -4,6 +4,7 @@ program at a conversion out of range, and compared with exact fractions."""
 import math
 import os
 import subprocess
+from decimal import Decimal, getcontext
 from fractions import Fraction
 
 import numpy as np
@@ -136,3 +137,33 @@ def test_steep_rows_keep_their_largest_logit_alone(placed):
             above = float(np.nextafter(np.float32(m), np.float32(INF)))
         answers = placed([(m, m, heat), (below, m, heat), (above, m, heat), (-INF, m, heat), (math.nan, m, heat)])
         assert [a[0] for a in answers] == [0, BINS, -1, BINS, BINS], (m, heat)
+
+
+@pytest.fixture(scope="module")
+def summed(tmp_path_factory):
+    """(r, n) -> the mantissa of r, and what a word to which n such tokens were added says of their count and sum."""
+    return program(tmp_path_factory, "summed", r"""
+int main() {
+    const Raise raise;
+    double r, n;
+    while (scanf("%la %la", &r, &n) == 2) {
+        uint64_t word = 0;
+        for (int i = 0; i < static_cast<int>(n); ++i) word += __builtin_bit_cast(uint64_t, raise(r));
+        printf("%a %d %a %a\n", mantissa_of(raise(r)), count_in(word), static_cast<double>(units_in(word)),
+               static_cast<double>(units_of(raise(r))));
+    }
+}
+""")
+
+
+def test_mantissas_and_their_sums(summed):
+    """A mantissa is within 2^-45.7 of 2^(r / 4), as a whole number of 2^-45; sums and counts of up to 1024 are exact."""
+    getcontext().prec = 40
+    g = np.random.default_rng(5)
+    cases = [(float(r), float(n)) for r in np.concatenate([[-0.5, 0.5, 0.0, -2.0 ** -60], g.uniform(-0.5, 0.5, 400)])
+             for n in (0, 1, 2, int(g.integers(3, 1024)), 1023, 1024)]
+    for (r, n), (mantissa, count, total, units) in zip(cases, summed(cases)):
+        want = (Decimal(2).ln() * Decimal(r) / 4).exp()
+        assert abs(Decimal(mantissa) / want - 1) <= Decimal(2.0 ** -45.7), r
+        assert units == mantissa * 2.0 ** 45 and units == int(units)
+        assert (count, total) == (n, n * units), (r, n)       # below 2^56: even where float64 rounds it alike
