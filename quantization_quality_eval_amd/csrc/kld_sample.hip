@@ -67,7 +67,10 @@ constexpr int kSplit = 256;         // parts of a bin, or of a range of logits
 constexpr int kFew = 64;            // tokens that a wave ranks
 constexpr int kMaxSlices = 512;     // of a row: what the draw knows of each is held in LDS
 constexpr double kLeast = 0x1p-64;  // smallest share of the likeliest token's weight that is kept
-constexpr int64_t kPassSlices = 32768;  // slices per pass over the workspace (at 19 a row 305 MB)
+// A pass over the workspace takes as many rows as fit in this many slices, and in this many bytes or as many as the
+// logits have, at least one: 32768 x 60 then ask for 232 MB, 8192 x 32000 bfloat16 for 0.4 GB instead of
+// the 4.5 and 1.2 that a list of kList tokens and no bound in bytes took, at 1.77 and 0.78 ms instead of 1.81 and 0.94.
+constexpr int64_t kPassSlices = 32768, kPassBytes = int64_t{1} << 28;
 // Sums that equal each other but for the order of their additions count as equal.
 constexpr double kSame = 0x1p-44;
 
@@ -95,13 +98,22 @@ struct Plan {
 struct Layout {
     Info* info;              // [rows][slices]
     Plan* plan;              // [rows]
-    Token* list;             // [rows][kList]
+    Token* list;             // [rows][list_of(vocab)]
     double* masses;          // [rows][slices][kBins]: a bin's sum of mantissas, in units
     uint16_t* counts;        // and its count
 };
 __host__ __device__ inline int64_t slices_of(int64_t vocab) { return (vocab + kSlice - 1) / kSlice; }
 constexpr int64_t kSliceBytes = sizeof(Info) + kBins * (sizeof(double) + sizeof(uint16_t));
-constexpr int64_t kRowBytes = sizeof(Plan) + kList * sizeof(Token);
+__host__ __device__ inline int64_t list_of(int64_t vocab) { return vocab < kList ? vocab : kList; }
+inline int64_t row_bytes(int64_t vocab) {
+    return slices_of(vocab) * kSliceBytes + static_cast<int64_t>(sizeof(Plan)) + list_of(vocab) * static_cast<int64_t>(sizeof(Token));
+}
+inline int64_t pass_rows(int type, int64_t vocab, int64_t n_rows) {
+    const int64_t bytes = std::max(kPassBytes, n_rows * vocab * (type == kF32 ? 4 : 2));
+    const int64_t most = std::max<int64_t>(1, std::min(kPassSlices / slices_of(vocab), bytes / row_bytes(vocab)));
+    const int64_t passes = (n_rows + most - 1) / most;
+    return passes > 1 ? (n_rows + passes - 1) / passes : std::max<int64_t>(1, n_rows);  // even ones
+}
 
 template <class E>
 struct Elem;
@@ -740,7 +752,7 @@ template <class E>
 __device__ __forceinline__ Row<E> row_of(const SampleArgs& a, const Layout& ws, int64_t row, int64_t here, int slices,
                                          Shared& sh) {
     return Row<E>{static_cast<const E*>(a.logits) + row * a.row_stride, static_cast<int>(a.vocab), slices,
-                  settings_of(a, row), Frame{}, ws.masses + here * slices * kBins, ws.counts + here * slices * kBins, ws.list + here * kList, 0, Raise(), sh};
+                  settings_of(a, row), Frame{}, ws.masses + here * slices * kBins, ws.counts + here * slices * kBins, ws.list + here * list_of(a.vocab), 0, Raise(), sh};
 }
 
 // The bin in which a row is cut first, and for each of its slices the logits that belong to it.
@@ -818,13 +830,13 @@ __global__ void __launch_bounds__(kScanThreads, 8) list_kernel(SampleArgs a, int
     put = from_lane(put, 63) + to - n;
     Frame frame{};
     if (first < last) frame = frame_of(value_of(best), settings_of(a, row).heat);
-    Token* list = ws.list + here * kList;
+    Token* list = ws.list + here * list_of(vocab);
     // a lane has few: they are read again rather than picked out of registers
     for (; mine; mine &= mine - 1, ++put) {
         const int id = held_id<E>(slice, vocab, __builtin_ctz(mine));
         const float z = Elem<E>::widen(in[id]);
         const int bin = first < last ? spot_of(z, frame).bin : last;
-        if (put < kList) list[put] = Token{order_of(z), static_cast<unsigned int>(id) << 9 | bin};
+        if (put < list_of(vocab)) list[put] = Token{order_of(z), static_cast<unsigned int>(id) << 9 | bin};
     }
 }
 
@@ -1034,12 +1046,12 @@ __global__ void __launch_bounds__(kDrawThreads, 4) draw_kernel(SampleArgs a, int
 template <class E>
 hipError_t launch(const SampleArgs& a, void* workspace, hipStream_t stream) {
     const int64_t slices = slices_of(a.vocab);
-    const int64_t rows = std::max<int64_t>(1, std::min(a.n_rows, kPassSlices / slices));
+    const int64_t rows = pass_rows(a.type, a.vocab, a.n_rows);
     Layout ws;
     ws.info = static_cast<Info*>(workspace);
     ws.plan = reinterpret_cast<Plan*>(ws.info + rows * slices);
     ws.list = reinterpret_cast<Token*>(ws.plan + rows);
-    ws.masses = reinterpret_cast<double*>(ws.list + rows * kList);
+    ws.masses = reinterpret_cast<double*>(ws.list + rows * list_of(a.vocab));
     ws.counts = reinterpret_cast<uint16_t*>(ws.masses + rows * slices * kBins);
     const bool limits = a.temperature.each || a.top_ks || a.top_p.each || a.min_p.each ||
                         (a.temperature.all > 0.0 &&
@@ -1060,9 +1072,8 @@ hipError_t launch(const SampleArgs& a, void* workspace, hipStream_t stream) {
 
 }  // namespace
 
-int64_t sample_workspace_bytes(int, int64_t vocab, int64_t n_rows) {
-    const int64_t slices = slices_of(vocab);
-    return std::max<int64_t>(1, std::min(n_rows, kPassSlices / slices)) * (slices * kSliceBytes + kRowBytes);
+int64_t sample_workspace_bytes(int type, int64_t vocab, int64_t n_rows) {
+    return pass_rows(type, vocab, n_rows) * row_bytes(vocab);
 }
 
 hipError_t launch_sample(const SampleArgs& a, void* workspace, hipStream_t stream) {

@@ -133,3 +133,23 @@ def test_random_draws_are_those_of_float64(rows, vocab, dtype):
         want, want_lp = oa.sample(synth.to_numpy_bits(z), u.cpu().numpy(), **s)
         assert np.array_equal(t.cpu().numpy(), want)
         assert (np.abs(lp.double().cpu().numpy() - want_lp) <= 2.0 ** -24 * np.abs(want_lp) + 2.0 ** -44).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,vocab", [(4500, 8192), (3001, 16385), (9001, 3000), (70001, 60)])
+def test_rows_of_several_passes(rows, vocab, dtype):
+    """More rows than one pass over the workspace holds: what a call for each few rows draws."""
+    need, one = qqe.sample_workspace_bytes(vocab, rows, dtype), qqe.sample_workspace_bytes(vocab, 1, dtype)
+    say(f"[sample] {rows} x {vocab} {dtype}: {need} bytes, {one} a row")
+    assert need < rows * one
+    g = torch.Generator(device=DEV).manual_seed(rows)
+    z = (torch.randn(rows, vocab, generator=g, device=DEV) * 3).to(TYPES[dtype])
+    u = torch.rand(rows, generator=g, device=DEV)
+    k = torch.randint(0, 400, (rows,), generator=g, device=DEV, dtype=torch.int32)
+    ws = torch.full((need + 256,), 255, dtype=torch.uint8, device=DEV)
+    t, lp = qqe.sample(z, u, top_k=k, top_p=0.9, workspace=ws[:need])
+    assert (ws[need:] == 255).all()
+    for r in range(0, rows, 997):
+        part = slice(r, min(r + 997, rows))
+        a, b = qqe.sample(z[part], u[part], top_k=k[part], top_p=0.9)
+        assert torch.equal(a, t[part]) and torch.equal(b, lp[part]), r
