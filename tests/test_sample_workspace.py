@@ -24,3 +24,11 @@ def test_workspace_of_ordinary_batches_holds_all_rows():
     for rows, vocab in ((1, 151936), (64, 151936), (1024, 151936), (512, 32000), (16384, 2000)):
         assert qqe.kld_eval_sample_workspace(vocab, 1, rows) == rows * qqe.kld_eval_sample_workspace(vocab, 1, 1) or (
             rows * qqe.kld_eval_sample_workspace(vocab, 1, 1) > PASS)
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("vocab", [1, 60, 3000, 8192, 16385, 32000, 151936, 1 << 22])
+def test_workspace_of_a_batch_serves_smaller_ones(vocab, dtype):
+    counts = sorted({int(1.07 ** i) for i in range(225)} | {1 << 22})
+    needs = [qqe.kld_eval_sample_workspace(vocab, dtype, n) for n in counts]
+    assert all(a <= b for a, b in zip(needs, needs[1:]))
