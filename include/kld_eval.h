@@ -627,7 +627,9 @@ kld_status kld_eval_matmul_int8(const int8_t* x, int64_t x_stride, const float* 
  * the kept w exceeds uniforms[r] times their whole sum; logp is the logarithm of
  * w over that sum, the log-probability with which it was drawn. Weights are formed
  * in float64 and rounded to 2^-45 of themselves, sums of them are exact or in float64,
- * and a sum that equals a border but for that counts as reaching it.
+ * and a sum that equals a border but for 2^-44 of itself counts as reaching it. Where no
+ * limit is set the whole sum may hold tokens below 2^-64 that are not drawn, 2^-42 of it
+ * at most.
  *   logits       device rows of `vocab` elements of dtype, row_stride elements
  *                apart (>= vocab); any alignment of the type; vocab and n_rows at most 4,194,304
  *   uniforms     float32[n_rows] in [0, 1): values outside are taken to its ends,

@@ -106,9 +106,10 @@ __device__ __forceinline__ void wait_fills() {
 // A workgroup's waves share 16 kCols columns and split the sum: each takes every
 // fourth block of 128 bytes of the weight rows and of x (out of the cache), and the
 // four partial sums meet in LDS. Nothing is shared before the end, so no wave waits for
-// another. Memory bounds it: 4 rows x 2048 by 151936 take 49 us, 6.4 TB/s of weights,
-// 1 x 4096 by 32000 27 us. Blocks of 256 bytes take 50 and 27, without the next block on
-// its way 59 and 29, with loads past the cache 57 and 27.
+// another. Memory bounds it: 4 rows x 2048 by 151936 take 49-51 us, 6.2 TB/s of weights,
+// 1 x 4096 by 32000 27 us (23 where the weights stay in the memory-side cache from one call to
+// the next). Blocks of 256 bytes take 50 and 27, without the next block on its way 59 and 29,
+// with loads past the cache 57 and 27.
 constexpr int kWaves = 4;
 constexpr int kSteps = 2;  // matrix instructions of 64 bytes each per block
 constexpr int kBlock = 64 * kSteps;
@@ -215,11 +216,14 @@ constexpr int kDepth = 64;  // bytes of a row per stage: one matrix instruction'
 // weight rows of 32 in fours, in turn; w's chunks are ordered so that those lie in all
 // banks.
 //
-// 8192 x 2048 by 151936 to bfloat16: 2.78 ms, 1.84 POP/s; 8192 x 8192 by 8192 465 us, 2.36
-// (a library's 8-bit product, unscaled, 1.94). At the latter the matrix units are busy for 65 %
-// of the cycles, at the former for 45 %: what is left there is the writing of 2.5 GB (without
-// it 2.28 ms). 32 x 2048 by 151936: 66 us, 4.7 TB/s of weights; 333 x 1000 by 32001 to float32,
-// 1000 bytes being no multiple of 16, 31 us by registers. Two stages of 128 bytes took 533 us at
+// 8192 x 2048 by 151936 to bfloat16: 2.74 ms, 1.86 POP/s; 8192 x 8192 by 8192 439 us, 2.50
+// (a library's 8-bit product, unscaled, 2.01). At the latter the matrix units are busy for 65 %
+// of the cycles, at the former for 43 %: what is left there is the writing of 2.5 GB (without
+// it 2.28 ms). 32 x 2048 by 151936, tiles of 64 x 128: 66 us, 4.7 TB/s of weights. 333 x 1000 by
+// 32001 to float32, rows 1024 bytes apart: 29.6 us, fifteen stages straight to LDS and the sixteenth
+// by registers, 252 tiles for 256 compute units that each begin with nothing in LDS and end in the
+// storing of 43 MB (matrix units busy for a third of the cycles); rows 1000 bytes apart, all by
+// registers, 44 us. Two stages of 128 bytes took 533 us at
 // 8192^3; one tile per workgroup 2.87 ms at the first size; four waves of 128 x 128 spill; stores past the cache take
 // 2.75 ms, but 3.45 instead of 3.14 for float32; workgroups started at different times 2.76, but 512 to 543 at 8192^3.
 //
@@ -526,14 +530,19 @@ hipError_t launch_tiles(const Int8Args& a, hipStream_t stream) {
 }
 
 // Up to 16 rows the weights' way from memory decides: straight into registers; wider columns
-// per wave where x is read often (16 x 4096 by 32000: 29 us, 31 with two; 4 x 2048 by 151936: 52,
-// 49 with two). So it does for 64 rows and few columns, where tiles would leave most of the chip
-// idle (64 x 4096 by 4096: 10 us, tiles 12; by 32000 it is 23, tiles 20).
+// per wave where x is read often (16 x 4096 by 32000: 23.7 us, 28.4 with two; 4 x 2048 by 151936:
+// 54.6, 51.5 with two). So it does for 64 rows and few columns, where tiles would leave much of the
+// chip idle (64 x 1024 by 1024 4.8 us, tiles of 64 x 64 5.6; 17 x 2048 by 8192 6.2, 7.4; 64 x 11008
+// by 4096 22, 29). At the rule's corner, many rows, columns and bytes at once, the tiles
+// win (64 x 4096 by 4096 11.3 us, 10.8; 64 x 2048 by 8192 10.4, 7.4; 48 x 8192 by 8192 33, 21), and
+// beyond it by far (64 x 4096 by 32000 59, 22).
 //
 // Among the tiles, the one whose workgroups take the least time: the steps of the compute unit
 // that gets the most of them, at what a step of each tile was measured to take there (1024 x 2048
-// by 32000, all units full). So 512 x 4096 by 4096 takes tiles of 64 x 128 (24 us; 128 x 128 27,
-// 256 x 256 51), 2000 x 1000 by 5000 of 256 x 256 (24 us; 128 x 128 29).
+// by 32000 to bfloat16, all units full). The results' width and the number of stages do not enter, since all
+// tiles write the same results and their steps grow alike with the stages. So 512 x 4096 by 4096 takes tiles of
+// 64 x 128 (16.9 us; 128 x 128 20.1, 256 x 256 45), 32 x 2048 by 151936 as well (65.6; 64 x 64 72.5), 333 x 1000 by
+// 32001 to float32 256 x 256 (29.6 us; 128 x 128 30.6, 64 x 128 35.4), 2000 x 1000 by 5000 too (24.4; 26.4, 27.9).
 template <class O>
 hipError_t launch(const Int8Args& a, hipStream_t stream) {
     if (a.n_rows <= 16)

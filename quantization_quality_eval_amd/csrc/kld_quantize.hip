@@ -12,10 +12,10 @@
 // A row is read once: each thread keeps its share in registers between the
 // maximum and the rounding (kHold units of eight elements; the units of longer rows
 // beyond those are read again, out of the cache). Memory bounds it: 32000 x 4096
-// bfloat16 (393 MB) 79-85 us, 4.6-4.9 TB/s, a large copy's rate; 8192 x 1001 float32 11 us,
-// one row of 4096 2.5 us in the kernel. Beside memory the rounding in float64, at half rate,
-// takes the most: the product and its first rounding are one fused operation (30000 x 2048:
-// 36 us, in two 41).
+// bfloat16 (393 MB) 81-87 us, 4.5-4.9 TB/s, a large copy's rate; 8192 x 1001 float32 11.7 us,
+// one row of 4096 2.4 us in the kernel. Beside memory the rounding in float64, at half rate,
+// takes the most: the product and its first rounding are one fused operation (in two, 30000 x 2048
+// took an eighth more).
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -160,9 +160,11 @@ hipError_t launch(const QuantizeArgs& a, hipStream_t stream) {
 }
 
 // Threads of a row: as many as it takes to hold it in few units each. Rows of up to 256 take a quarter of
-// a wave, the rest of whose lanes would idle (309697 x 116 bfloat16: 40 us, with a wave each 139); up to 2048 a
-// wave that waits for no other (40000 x 1040: 39 us, with the workgroup 54; 30000 x 2048: 41, 45). Above, eight
-// units in a wave leave room for too few waves (32000 x 4096: 138 us, with the workgroup 82).
+// a wave, the rest of whose lanes would idle (309697 x 116 bfloat16: 47-54 us, with a wave each 129); up to 2048 a
+// wave that waits for no other (40000 x 1040: 34-42 us, with the workgroup 58-71; 30000 x 2048: 35-37, 52). Above,
+// eight units in a wave leave room for too few waves (32000 x 4096: 140 us, with the workgroup 83; 30000 x 2064: 70,
+// 57). Widths between these steps leave lanes idle: 384 moves 3.1 TB/s, 513 2.5, 2064 3.2 and 4112 3.6, where 2048 and
+// 4096 move 4.7 to 5.0.
 template <class E>
 hipError_t launch_type(const QuantizeArgs& a, hipStream_t stream) {
     if (a.dim <= 16 * kUnit) return launch<E, 16, 1>(a, stream);

@@ -26,23 +26,30 @@
 //   draw  a workgroup per row: cuts the bins by top-k, then top-p, within a bin by a histogram
 //         of 256 parts and then by ranking the last 64 tokens; sums what each slice keeps, finds
 //         the slice that holds the draw, reads it and draws from it.
-// Rows that no limit cuts need the scan and the draw alone.
+// Rows that no limit cuts need the scan and the draw alone: there a slice's sum holds what lies between 2^-64 of
+// the largest weight and the last bin's 2^-68 as well, 2^-42 of a row's sum at most, though it is never drawn.
 //
-// 1024 x 151936 bfloat16 (311 MB), limits of every kind: scan 117 us, plan 13, list 48, draw 69,
-// and 262 us in all; the memory could give the row once in 46 us. The scan is bound by float64
-// arithmetic, which runs at half rate here: about 108 cycles of a SIMD for each 64 tokens, of
-// which 7 multiply-adds raise and 3 operations place a token; its LDS atomics and loads
-// (2.7 TB/s) fit beside that. Float32 would be faster, but its sums err
-// by more than the weight of a token near the border of a long row. The list is bound by its second reading of the rows
-// (6.5 TB/s). The draw is bound by latency: two
-// workgroups to a CU, each a chain of reductions and barriers. 64 rows take 28 us without limits
-// and 40 to 70 with them, one row of 32000 tokens 34 us: the four launches' own latencies
-// (5, 5, 3 and 13 us).
+// 1024 x 151936 bfloat16 (311 MB), top-p: scan 129 us, plan 14, list 43, draw 71, and 238 us in all
+// among other calls; the memory could give the row once in 46 us. The scan is bound by float64
+// arithmetic, which runs at half rate here: for each 64 tokens of a SIMD 12 operations of it, of
+// which 7 multiply-adds raise a token, beside 5 others and an LDS atomic (2.4 TB/s; its LDS holds
+// bank conflicts for a fifth of its cycles). Float32 would be faster, but its sums err
+// by more than the weight of a token near the border of a long row. The list is bound by its second reading of the
+// rows (7 TB/s; 218 of the 311 MB come from memory). The draw is bound by latency: two
+// workgroups to a CU, each a chain of reductions and barriers. Without limits the 1024 rows take 158 us (scan 127,
+// draw 31), at temperature 0 56 (scan 47, memory's rate, draw 8). 64 rows take 27 us without limits
+// and 40 to 60 with them, one row of 32000 tokens 35 us: the four launches' own latencies
+// (5, 5, 5 and 20 us).
+//
+// Where a bin that is cut holds more than kList tokens, or top-p cuts one behind a top-k prefix longer than that,
+// the draw reads it from the row, slice after slice, in a workgroup by itself: 64 x 151936 with top-p take 200 us at
+// a spread of 0.3, 210 with a top-k of 50000 at a spread of 1, and 1.74 ms where all logits are equal, since every
+// token then adds to one LDS word; a row of 4194304 equal ones 47 ms.
 //
 // Measured on the way, 1024 x 151936: bins of a whole unit, whose tokens the draw looked for in
 // the rows by itself, 590 us; of a quarter, with two draws to a CU, 340; a list by a workgroup
 // per slice 97 to 72 us for 64 rows, in memory rather than in the draw's LDS 320 to 290. A draw of
-// 1024 threads was slower, 8 copies of the bins in LDS instead of 4 changed nothing.
+// 1024 threads was slower.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -220,8 +227,8 @@ __device__ __forceinline__ double weight(const Raise& raise, Spot at) { return m
 
 // ---- the scan ----
 
-// Left to itself with its registers (56, 92 for float32): kept to 64 it took 69 us instead of 65 for 512 x 151936
-// float32.
+// Left to itself with its registers (89, 92 for float32): kept to 64 it took 139 us instead of 136 at 1024 x 151936
+// bfloat16, 331 instead of 229 at 8192 x 32000.
 template <class E>
 __global__ void __launch_bounds__(kScanThreads) scan_kernel(SampleArgs a, int64_t first_row, Layout out, int slices) {
     __shared__ unsigned long long bins[(kBins + 1) * kCopies];
