@@ -75,8 +75,9 @@ constexpr int kFew = 64;            // tokens that a wave ranks
 constexpr int kMaxSlices = 512;     // of a row: what the draw knows of each is held in LDS
 constexpr double kLeast = 0x1p-64;  // smallest share of the likeliest token's weight that is kept
 // A pass over the workspace takes as many rows as fit in this many slices, and in this many bytes or as many as the
-// logits have, at least one: 32768 x 60 then ask for 232 MB, 8192 x 32000 bfloat16 for 0.5 GB instead of
-// the 4.5 and 1.2 that a list of kList tokens and no bound in bytes took, at 1.77 and 0.78 ms instead of 1.81 and 0.94.
+// logits have in bfloat16 (the same for float32, so that one workspace serves either type), at least one. So
+// 32768 x 60 ask for 232 MB and 8192 x 32000 for 0.5 GB, instead of the 4.5 and 1.2 GB that lists of kList tokens for
+// every row and no bound in bytes took, at 1.77 and 0.78 ms instead of 1.81 and 0.94.
 constexpr int64_t kPassSlices = 32768, kPassBytes = int64_t{1} << 28;
 // Sums that equal each other but for the order of their additions count as equal.
 constexpr double kSame = 0x1p-44;
@@ -116,8 +117,8 @@ inline int64_t row_bytes(int64_t vocab) {
     return slices_of(vocab) * kSliceBytes + static_cast<int64_t>(sizeof(Plan)) + list_of(vocab) * static_cast<int64_t>(sizeof(Token));
 }
 // How many rows the workspace holds: more for more rows, so that one that serves a batch serves a smaller one.
-inline int64_t held_rows(int type, int64_t vocab, int64_t n_rows) {
-    const int64_t bytes = std::max(kPassBytes, n_rows * vocab * (type == kF32 ? 4 : 2));
+inline int64_t held_rows(int64_t vocab, int64_t n_rows) {
+    const int64_t bytes = std::max(kPassBytes, n_rows * vocab * 2);
     return std::max<int64_t>(1, std::min({n_rows, kPassSlices / slices_of(vocab), bytes / row_bytes(vocab)}));
 }
 
@@ -1052,7 +1053,7 @@ __global__ void __launch_bounds__(kDrawThreads, 4) draw_kernel(SampleArgs a, int
 template <class E>
 hipError_t launch(const SampleArgs& a, void* workspace, hipStream_t stream) {
     const int64_t slices = slices_of(a.vocab);
-    const int64_t most = held_rows(a.type, a.vocab, a.n_rows), passes = (a.n_rows + most - 1) / most;
+    const int64_t most = held_rows(a.vocab, a.n_rows), passes = (a.n_rows + most - 1) / most;
     const int64_t rows = (a.n_rows + passes - 1) / passes;  // passes of even size
     Layout ws;
     ws.info = static_cast<Info*>(workspace);
@@ -1079,8 +1080,8 @@ hipError_t launch(const SampleArgs& a, void* workspace, hipStream_t stream) {
 
 }  // namespace
 
-int64_t sample_workspace_bytes(int type, int64_t vocab, int64_t n_rows) {
-    return held_rows(type, vocab, n_rows) * row_bytes(vocab);
+int64_t sample_workspace_bytes(int, int64_t vocab, int64_t n_rows) {
+    return held_rows(vocab, n_rows) * row_bytes(vocab);
 }
 
 hipError_t launch_sample(const SampleArgs& a, void* workspace, hipStream_t stream) {

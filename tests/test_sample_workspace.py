@@ -15,6 +15,7 @@ def test_workspace_is_in_proportion(rows, vocab, dtype):
     need = qqe.kld_eval_sample_workspace(vocab, dtype, rows)
     one = qqe.kld_eval_sample_workspace(vocab, dtype, 1)
     assert 0 < one <= need <= max(PASS, rows * vocab * SIZES[dtype], one)
+    assert need == qqe.kld_eval_sample_workspace(vocab, 1 - dtype, rows)      # one workspace serves either type
     # a row: its slices' bins, its own, and a list of no more tokens than it has
     assert one <= -(-vocab // 8192) * 3000 + 4000 + 8 * min(vocab, 16384)
     assert need == qqe.sample_workspace_bytes(vocab, rows, ("f32", "bf16")[dtype])
