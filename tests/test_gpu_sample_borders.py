@@ -153,3 +153,31 @@ def test_rows_of_several_passes(rows, vocab, dtype):
         part = slice(r, min(r + 997, rows))
         a, b = qqe.sample(z[part], u[part], top_k=k[part], top_p=0.9)
         assert torch.equal(a, t[part]) and torch.equal(b, lp[part]), r
+
+
+def test_captured_draws_of_several_passes():
+    """A graph whose passes share the workspace, replayed with other logits, eager work between the replays."""
+    rows, vocab = 4500, 8192
+    g = torch.Generator(device=DEV).manual_seed(11)
+    z, u = torch.empty((rows, vocab), dtype=torch.bfloat16, device=DEV), torch.empty(rows, device=DEV)
+    out = (torch.empty(rows, dtype=torch.int32, device=DEV), torch.empty(rows, device=DEV))
+    ws = torch.full((qqe.sample_workspace_bytes(vocab, rows),), 255, dtype=torch.uint8, device=DEV)
+    s = dict(temperature=0.8, top_k=300, top_p=0.9, min_p=0.01)
+
+    def fill():
+        z.copy_(torch.randn(rows, vocab, generator=g, device=DEV) * 3)
+        u.copy_(torch.rand(rows, generator=g, device=DEV))
+
+    fill()
+    qqe.sample(z, u, out=out, workspace=ws, **s)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        qqe.sample(z, u, out=out, workspace=ws, **s)
+    for _ in range(4):
+        fill()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [o.clone() for o in out]
+        want = qqe.sample(z, u, **s)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
