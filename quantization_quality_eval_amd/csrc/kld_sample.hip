@@ -20,7 +20,7 @@
 //         each of its upper 272 bins (68 binary units; what lies below 2^-64 of the largest
 //         weight is dropped), by LDS atomics;
 //   plan  a workgroup per row: adds the slices' bins up, finds the bin in which the order is
-//         cut first, and for each slice the logits that belong to that bin, by bisection;
+//         cut first, the logits that belong to that bin, by bisection, and the slices that hold any;
 //   list  a workgroup per slice: the tokens between those logits, compared as floats, to a
 //         list in memory (at most 16384 a row; a fuller bin is read from the row again);
 //   draw  a workgroup per row: cuts the bins by top-k, then top-p, within a bin by a histogram
@@ -32,8 +32,8 @@
 // 1024 x 151936 bfloat16 (311 MB), top-p: scan 129 us, plan 14, list 43, draw 71, and 238 us in all
 // among other calls; the memory could give the row once in 46 us. The scan is bound by float64
 // arithmetic, which runs at half rate here: for each 64 tokens of a SIMD 12 operations of it, of
-// which 7 multiply-adds raise a token, beside 5 others and an LDS atomic (2.4 TB/s; its LDS holds
-// bank conflicts for a fifth of its cycles). Float32 would be faster, but its sums err
+// which 7 multiply-adds raise a token, beside 5 others and an LDS atomic (2.4 TB/s; bank
+// conflicts take a fifth of the LDS' cycles). Float32 would be faster, but its sums err
 // by more than the weight of a token near the border of a long row. The list is bound by its second reading of the
 // rows (7 TB/s; 218 of the 311 MB come from memory). The draw is bound by latency: two
 // workgroups to a CU, each a chain of reductions and barriers. Without limits the 1024 rows take 158 us (scan 127,
@@ -762,7 +762,7 @@ __device__ __forceinline__ Row<E> row_of(const SampleArgs& a, const Layout& ws, 
                   settings_of(a, row), Frame{}, ws.masses + here * slices * kBins, ws.counts + here * slices * kBins, ws.list + here * list_of(a.vocab), 0, Raise(), sh};
 }
 
-// The bin in which a row is cut first, and for each of its slices the logits that belong to it.
+// The bin in which a row is cut first, the logits that belong to it and the slices that hold any.
 template <class E>
 __global__ void __launch_bounds__(kDrawThreads) plan_kernel(SampleArgs a, int64_t first_row, Layout ws, int slices) {
     __shared__ Shared sh;
